@@ -57,6 +57,25 @@ SIGNATURES = {
     "qlin_last_hip_error": (_S, []),
 }
 
+# include/qlin_w4.h: 4-bit weights, routing, experts
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
+_F = ctypes.c_float
+SIGNATURES_W4 = {
+    "qlin_w4_packed_bytes": (_I64, [_I64, _I64]),
+    "qlin_pack_w4": (_S, [_P, _I64, _I64, _I64, _P, _P]),
+    "qlin_linear_w4": (_S, [_P, _I64, _I64, _I32, _P, _P, _I32, _S, _P]),
+    "qlin_linear_swiglu_w4": (_S, [_P, _I64, _I64, _I32, _P, _P, _P, _P]),
+    "qlin_route": (_S, [_P, _S, _I64, _I64, _I32, _S, _P, _I32, _I32, _I32, _I32, _F, _P, _P, _P]),
+    "qlin_experts_w4_workspace": (_I64, [_I64, _I32, _I64, _I64, _I64]),
+    "qlin_experts_w4": (_S, [_P, _I64, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
+}
+
+
+class QlinW4Weight(ctypes.Structure):
+    """struct qlin_w4_weight: one packed 4-bit matrix, or one per expert."""
+    _fields_ = [("q_w", ctypes.c_void_p), ("s_w", ctypes.c_void_p), ("z_w", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
 
 class QlinSegment(ctypes.Structure):
     """struct qlin_segment: one weight matrix reading the call's activations."""
@@ -81,7 +100,7 @@ def _load():
             f"{LIB_PATH} is missing: build it with `python quantized_linear_layers_token_amd/build.py` "
             "(the HIP library is the only implementation; there is no fallback)")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **SIGNATURES_W4}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
@@ -333,3 +352,164 @@ def qlin_linear_swiglu(scheme, x, gate, up, h, q_x=None, s_x=None, stream=None):
           ("s_x", s_x, 4 * _sx_count(block, M, K), 4), ("x", x, 0, None))
     _check(_lib.qlin_linear_swiglu(scheme, _ptr(x), M, K, _ptr(gq), _ptr(gs), _ptr(uq), _ptr(us), gq.shape[0],
                                    _ptr(h), _ptr(q_x), _ptr(s_x), _stream(stream)), "qlin_linear_swiglu")
+
+
+# --------------------------------------------------------------------------
+# 4-bit weights, routing and experts (include/qlin_w4.h)
+#
+# These calls run on the device of their first tensor, whichever device is
+# current, on `stream` or that device's current stream.
+# --------------------------------------------------------------------------
+
+class W4Weight:
+    """4-bit weights laid out for the library (qlin_pack_w4): one matrix
+    [N, K], or `experts` of them.  Holds the packed codes and the scales and
+    zero points it was made with (they are used in place)."""
+
+    def __init__(self, packed, scales, zeros, experts, N, K, group):
+        self.packed, self.scales, self.zeros = packed, scales, zeros
+        self.experts, self.N, self.K, self.group = experts, N, K, group
+        self.device = packed.device
+        self._struct = QlinW4Weight(packed.data_ptr(), scales.data_ptr(), _ptr(zeros), N)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _launch(name, device, stream, *args):
+    import torch
+    if device.type != "cuda":
+        raise ValueError("the tensors must be device tensors")
+    index = device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    fn = getattr(_lib, name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != QLIN_OK:
+        raise QlinError(status, name)
+
+
+def _w4_tensor(t, name, shape, size, device):
+    """One tensor argument of the calls below: exactly this shape (None: any), contiguous, on the call's device."""
+    if not t.is_contiguous() or t.element_size() != size or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a contiguous tensor of {size}-byte elements"
+                         + (f" and shape {list(shape)}, not {list(t.shape)}" if shape is not None else ""))
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+
+
+def qlin_pack_w4(q_w, s_w, z_w=None, stream=None):
+    """q_w uint8 [N, K/2] (input 2 i in the low half of byte i) or [E, N, K/2],
+    s_w bf16 [.., N, K/group], z_w uint8 like s_w or None (8) -> W4Weight.
+    The packed codes are a new tensor; q_w need not be kept."""
+    import torch
+    if q_w.dim() not in (2, 3) or s_w.dim() != q_w.dim():
+        raise ValueError("q_w must be [N, K/2] or [E, N, K/2], s_w [N, K/group] or [E, N, K/group]")
+    E, N, K = (q_w.shape[0] if q_w.dim() == 3 else 1), q_w.shape[-2], 2 * q_w.shape[-1]
+    groups = s_w.shape[-1]
+    group = K // groups if groups else 0
+    if group not in (32, 64, 128) or group * groups != K:
+        raise ValueError(f"{groups} scales for {K} inputs: the group must be 32, 64 or 128 inputs")
+    _w4_tensor(q_w, "q_w", None, 1, q_w.device)
+    _w4_tensor(s_w, "s_w", (*q_w.shape[:-1], groups), 2, q_w.device)
+    if z_w is not None:
+        _w4_tensor(z_w, "z_w", (*q_w.shape[:-1], groups), 1, q_w.device)
+    size = _lib.qlin_w4_packed_bytes(N, K)
+    if (N and not size) or E > MAX_EXPERTS:
+        raise QlinError(QLIN_ERR_SHAPE, "qlin_pack_w4")
+    packed = torch.empty((E * size,), dtype=torch.uint8, device=q_w.device)
+    _launch("qlin_pack_w4", q_w.device, stream, q_w.data_ptr(), E, N, K, packed.data_ptr())
+    return W4Weight(packed, s_w, z_w, E, N, K, group)
+
+
+def _w4_input(x, w, name):
+    if x.dim() != 2 or not x.is_contiguous() or x.element_size() != 2:
+        raise ValueError("x must be a contiguous 2-D tensor of 2-byte elements")
+    if w.K != x.shape[1] or w.device != x.device:
+        raise ValueError(f"{name} has {w.K} inputs on {w.device}, x {x.shape[1]} on {x.device}")
+
+
+def qlin_linear_w4(x, segments, out=OUT_BF16, stream=None):
+    """x bf16 [M, K]; segments: list of (W4Weight [n, K], y [M, n]) sharing x, of one group size."""
+    M, K = x.shape
+    nw = len(segments)
+    weights, ys = (QlinW4Weight * nw)(), (_P * nw)()
+    size = _out_bytes(out)
+    for i, (w, y) in enumerate(segments):
+        _w4_input(x, w, f"segment {i}")
+        if w.experts != 1 or w.group != segments[0][0].group:
+            raise ValueError("every segment must be one matrix, all of one group size")
+        _w4_tensor(y, f"segment {i} y", (M, w.N), size, x.device)
+        weights[i] = w._struct
+        ys[i] = y.data_ptr()
+    _launch("qlin_linear_w4", x.device, stream, x.data_ptr(), M, K, segments[0][0].group if nw else 128, weights, ys, nw, out)
+
+
+def qlin_linear_swiglu_w4(x, gate, up, h, stream=None):
+    """x bf16 [M, K]; gate, up: W4Weight [I, K]; h bf16 [M, I] receives silu(x gate^T) * (x up^T), rounded once."""
+    _w4_input(x, gate, "gate")
+    _w4_input(x, up, "up")
+    M, K = x.shape
+    if gate.experts != 1 or up.experts != 1 or gate.N != up.N or gate.group != up.group:
+        raise ValueError("gate and up must be one matrix each, of one shape and group size")
+    _w4_tensor(h, "h", (M, gate.N), 2, x.device)
+    _launch("qlin_linear_swiglu_w4", x.device, stream, x.data_ptr(), M, K, gate.group, gate._ref, up._ref, h.data_ptr())
+
+
+def qlin_route(logits, ids, weights, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, group_best=2,
+               renormalize=True, scale=1.0, stream=None):
+    """logits bf16 or f32 [T, E]; ids int32 [T, k] and weights f32 [T, k] receive the k experts of each token."""
+    import torch
+    if logits.dim() != 2 or not logits.is_contiguous() or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits must be a contiguous 2-D tensor of bfloat16 or float32")
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("ids must be int32 [T, k] and weights float32 [T, k]")
+    k = ids.shape[1]
+    _w4_tensor(ids, "ids", None, 4, logits.device)
+    _w4_tensor(weights, "weights", (T, k), 4, logits.device)
+    if bias is not None:
+        if bias.dtype != torch.float32:
+            raise ValueError("bias must be float32 [E]")
+        _w4_tensor(bias, "bias", (E,), 4, logits.device)
+    _launch("qlin_route", logits.device, stream, logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, T, E,
+            k, score, _ptr(bias), groups, top_groups, group_best, 1 if renormalize else 0, scale, ids.data_ptr(),
+            weights.data_ptr())
+
+
+def qlin_experts_w4_workspace(T, k, gate, up, down):
+    """Bytes of qlin_experts_w4's workspace for T tokens of k experts each."""
+    size = _lib.qlin_experts_w4_workspace(T, k, gate.experts, gate.K, gate.N)
+    if not size and T:
+        raise QlinError(QLIN_ERR_SHAPE, "qlin_experts_w4_workspace")
+    return size
+
+
+def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
+    """x bf16 [T, H]; ids int32 [T, k] (outside 0..E-1: no expert), weights f32 [T, k]; gate, up: W4Weight of E
+    matrices [I, H], down of E matrices [H, I]; y bf16 [T, H]; workspace uint8, qlin_experts_w4_workspace bytes."""
+    import torch
+    _w4_input(x, gate, "gate")
+    T, H = x.shape
+    E, I, group = gate.experts, gate.N, gate.group
+    if (up.experts, up.N, up.K, up.group) != (E, I, H, group) or (down.experts, down.N, down.K, down.group) != (E, H, I, group):
+        raise ValueError("up must have gate's shape, down be [E, H, I], all of one group size")
+    if up.device != x.device or down.device != x.device:
+        raise ValueError(f"every tensor must be on {x.device}")
+    if ids.dim() != 2 or ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("ids must be int32 [T, k] and weights float32 [T, k]")
+    k = ids.shape[1]
+    device = x.device
+    _w4_tensor(ids, "ids", (T, k), 4, device)
+    _w4_tensor(weights, "weights", (T, k), 4, device)
+    _w4_tensor(y, "y", (T, H), 2, device)
+    _w4_tensor(workspace, "workspace", None, 1, device)
+    need = _lib.qlin_experts_w4_workspace(T, k, E, H, I)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
+    _launch("qlin_experts_w4", device, stream, x.data_ptr(), T, H, I, E, k, group, ids.data_ptr(), weights.data_ptr(),
+            gate._ref, up._ref, down._ref, y.data_ptr(), workspace.data_ptr())

@@ -6,8 +6,20 @@
 #include "qlin_internal.h"
 
 namespace {
-
 thread_local int g_last_hip_error = 0;
+}
+
+namespace qlin {
+
+qlin_status hip_status(hipError_t e) {
+    if (e == hipSuccess) return QLIN_OK;
+    g_last_hip_error = (int)e;
+    return QLIN_ERR_HIP;
+}
+
+}  // namespace qlin
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -20,11 +32,7 @@ Range rng(const void* p, int64_t bytes) {
 }
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
-qlin_status hip_status(hipError_t e) {
-    if (e == hipSuccess) return QLIN_OK;
-    g_last_hip_error = (int)e;
-    return QLIN_ERR_HIP;
-}
+using qlin::hip_status;
 
 bool valid_k(int64_t K) { return K > 0 && (K % 16) == 0 && K <= QLIN_MAX_K; }
 bool valid_mn(int64_t v) { return v >= 0 && v <= QLIN_MAX_MN; }

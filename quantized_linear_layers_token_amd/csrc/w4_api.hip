@@ -1,0 +1,283 @@
+// C ABI of the 4-bit products, the router and the experts' MLP: argument
+// validation and dispatch.  No allocation, no synchronization; every check
+// runs before the first launch.
+#include <stdint.h>
+
+#include "../../include/qlin_w4.h"
+#include "qlin_internal.h"
+#include "w4_internal.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Range {
+    uintptr_t lo, hi;
+};
+Range rng(const void* p, int64_t bytes) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return Range{b, b + (uintptr_t)bytes};
+}
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+
+bool valid_mn(int64_t v) { return v >= 0 && v <= QLIN_MAX_MN; }
+bool valid_k(int64_t K) { return K > 0 && K % 32 == 0 && K <= QLIN_MAX_K; }
+bool valid_group(int32_t g, int64_t K) { return (g == 32 || g == 64 || g == 128) && K % g == 0; }
+
+// Ranges that a weight of E matrices [n, K] covers.
+struct WeightRanges {
+    Range q, s, z;
+};
+WeightRanges ranges(const qlin_w4_weight& w, int64_t E, int64_t K, int32_t group) {
+    const int64_t scales = E * w.n * (K / group);
+    return WeightRanges{rng(w.q_w, E * qlin_w4_packed_bytes(w.n, K)), rng(w.s_w, 2 * scales), rng(w.z_w, w.z_w ? scales : 0)};
+}
+bool overlap(Range a, const WeightRanges& w) { return overlap(a, w.q) || overlap(a, w.s) || overlap(a, w.z); }
+
+qlin_status check_pointers(const qlin_w4_weight& w) {
+    if (!w.q_w || !w.s_w) return QLIN_ERR_NULL;
+    if (!aligned(w.q_w, 16) || !aligned(w.s_w, 2)) return QLIN_ERR_ALIGN;
+    return QLIN_OK;
+}
+
+// Outputs and inputs of one call stay within what an address space holds, so
+// that no size computed from them overflows.
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+}  // namespace
+
+extern "C" {
+
+int64_t qlin_w4_packed_bytes(int64_t N, int64_t K) {
+    if (!valid_mn(N) || !valid_k(K)) return 0;
+    return qlin::w4_row_tiles(N) * qlin::w4_k_tiles(K) * qlin::kW4Block;
+}
+
+qlin_status qlin_pack_w4(const uint8_t* q_w, int64_t E, int64_t N, int64_t K, uint8_t* q_w_packed, hipStream_t stream) {
+    if (E < 0 || E > QLIN_MAX_EXPERTS || !valid_mn(N) || !valid_k(K)) return QLIN_ERR_SHAPE;
+    if (E == 0 || N == 0) return QLIN_OK;
+    if (!q_w || !q_w_packed) return QLIN_ERR_NULL;
+    if (!aligned(q_w, 16) || !aligned(q_w_packed, 16)) return QLIN_ERR_ALIGN;
+    if (overlap(rng(q_w, E * N * (K / 2)), rng(q_w_packed, E * qlin_w4_packed_bytes(N, K)))) return QLIN_ERR_ALIAS;
+    return qlin::hip_status(qlin::launch_pack_w4(q_w, E, N, K, q_w_packed, stream));
+}
+
+qlin_status qlin_linear_w4(const uint16_t* x, int64_t M, int64_t K, int32_t group, const qlin_w4_weight* weights,
+                           void* const* y, int32_t nw, qlin_out out, hipStream_t stream) {
+    if (!weights || !y) return QLIN_ERR_NULL;
+    if (nw < 1 || nw > QLIN_MAX_SEGMENTS) return QLIN_ERR_SHAPE;
+    if (!valid_mn(M) || !valid_k(K) || !valid_group(group, K)) return QLIN_ERR_SHAPE;
+    if (out != QLIN_OUT_BF16 && out != QLIN_OUT_F32) return QLIN_ERR_UNSUPPORTED;
+    int64_t rows = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (!valid_mn(weights[i].n)) return QLIN_ERR_SHAPE;
+        rows += weights[i].n;
+    }
+    if (rows > QLIN_MAX_MN || M * rows > kMaxElements) return QLIN_ERR_SHAPE;
+    if (M == 0 || rows == 0) return QLIN_OK;
+    if (!x) return QLIN_ERR_NULL;
+    if (!aligned(x, 16)) return QLIN_ERR_ALIGN;
+    qlin::W4Call c{};
+    c.x = x;
+    c.mode = (int)out;
+    c.group = group;
+    c.M = M;
+    c.K = K;
+    const Range rx = rng(x, 2 * M * K);
+    const int64_t size = out == QLIN_OUT_F32 ? 4 : 2;
+    for (int i = 0; i < nw; ++i) {
+        if (weights[i].n == 0) continue;
+        const qlin_status st = check_pointers(weights[i]);
+        if (st != QLIN_OK) return st;
+        if (!y[i]) return QLIN_ERR_NULL;
+        if (!aligned(y[i], 16)) return QLIN_ERR_ALIGN;
+        const Range ry = rng(y[i], size * M * weights[i].n);
+        if (overlap(ry, rx)) return QLIN_ERR_ALIAS;
+        for (int j = 0; j < nw; ++j) {
+            if (weights[j].n == 0) continue;
+            if (overlap(ry, ranges(weights[j], 1, K, group))) return QLIN_ERR_ALIAS;
+            if (j != i && y[j] && overlap(ry, rng(y[j], size * M * weights[j].n))) return QLIN_ERR_ALIAS;
+        }
+        c.w[c.nseg] = weights[i].q_w;
+        c.s[c.nseg] = weights[i].s_w;
+        c.z[c.nseg] = weights[i].z_w;
+        c.y[c.nseg] = y[i];
+        c.n[c.nseg] = (int)weights[i].n;
+        ++c.nseg;
+    }
+    return qlin::hip_status(qlin::launch_w4_stream(c, false, false, stream));
+}
+
+qlin_status qlin_linear_swiglu_w4(const uint16_t* x, int64_t M, int64_t K, int32_t group, const qlin_w4_weight* gate,
+                                  const qlin_w4_weight* up, uint16_t* h, hipStream_t stream) {
+    if (!gate || !up) return QLIN_ERR_NULL;
+    if (!valid_mn(M) || !valid_k(K) || !valid_group(group, K)) return QLIN_ERR_SHAPE;
+    const int64_t I = gate->n;
+    if (!valid_mn(I) || up->n != I || 2 * I > QLIN_MAX_MN || M * I > kMaxElements) return QLIN_ERR_SHAPE;
+    if (M == 0 || I == 0) return QLIN_OK;
+    if (!x || !h) return QLIN_ERR_NULL;
+    for (const qlin_w4_weight* w : {gate, up}) {
+        const qlin_status st = check_pointers(*w);
+        if (st != QLIN_OK) return st;
+    }
+    if (!aligned(x, 16) || !aligned(h, 16)) return QLIN_ERR_ALIGN;
+    const Range rh = rng(h, 2 * M * I);
+    if (overlap(rh, rng(x, 2 * M * K)) || overlap(rh, ranges(*gate, 1, K, group)) || overlap(rh, ranges(*up, 1, K, group)))
+        return QLIN_ERR_ALIAS;
+    qlin::W4Call c{};
+    c.x = x;
+    c.w[0] = gate->q_w, c.w[1] = up->q_w;
+    c.s[0] = gate->s_w, c.s[1] = up->s_w;
+    c.z[0] = gate->z_w, c.z[1] = up->z_w;
+    c.y[0] = h;
+    c.n[0] = c.n[1] = (int)I;
+    c.nseg = 2;
+    c.mode = QLIN_OUT_BF16;
+    c.group = group;
+    c.M = M;
+    c.K = K;
+    return qlin::hip_status(qlin::launch_w4_stream(c, true, false, stream));
+}
+
+qlin_status qlin_route(const void* logits, qlin_out logits_type, int64_t T, int64_t E, int32_t k, qlin_score score,
+                       const float* bias, int32_t groups, int32_t top_groups, int32_t group_best, int32_t renormalize,
+                       float scale, int32_t* ids, float* weights, hipStream_t stream) {
+    if (logits_type != QLIN_OUT_BF16 && logits_type != QLIN_OUT_F32) return QLIN_ERR_UNSUPPORTED;
+    if (score != QLIN_SCORE_SOFTMAX && score != QLIN_SCORE_SIGMOID) return QLIN_ERR_UNSUPPORTED;
+    if (!valid_mn(T) || E < 1 || E > QLIN_MAX_EXPERTS) return QLIN_ERR_SHAPE;
+    if (groups < 1 || groups > QLIN_MAX_GROUPS || E % groups != 0 || top_groups < 1 || top_groups > groups) return QLIN_ERR_SHAPE;
+    if (group_best < 1 || group_best > 2) return QLIN_ERR_SHAPE;
+    if (k < 1 || k > QLIN_MAX_CHOICES || k > top_groups * (E / groups)) return QLIN_ERR_SHAPE;
+    if (T == 0) return QLIN_OK;
+    if (!logits || !ids || !weights) return QLIN_ERR_NULL;
+    if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return QLIN_ERR_ALIGN;
+    const Range rl = rng(logits, T * E * (logits_type == QLIN_OUT_F32 ? 4 : 2)), rb = rng(bias, bias ? 4 * E : 0);
+    const Range ri = rng(ids, 4 * T * k), rw = rng(weights, 4 * T * k);
+    if (overlap(ri, rl) || overlap(rw, rl) || overlap(ri, rb) || overlap(rw, rb) || overlap(ri, rw)) return QLIN_ERR_ALIAS;
+    return qlin::hip_status(qlin::launch_route(logits, logits_type == QLIN_OUT_F32, T, (int)E, k, (int)score, bias, groups,
+                                               top_groups, group_best, renormalize != 0, scale, ids, weights, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The experts' workspace, every part 16-byte aligned.
+struct Workspace {
+    int64_t order, items, nitems, h, rows, bytes;
+};
+constexpr int64_t kDirectSlots = 32;     // routed rows that are multiplied one by one, without sorting
+
+int block_rows(int64_t slots, int64_t E) {
+    const int64_t per = slots / E;       // rows of an expert, if they are spread evenly
+    return per <= 8 ? 16 : per <= 24 ? 32 : 64;
+}
+int64_t max_items(int64_t slots, int64_t E, int rows) { return (slots < E ? slots : E) + slots / rows; }
+
+Workspace layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+    const int64_t slots = T * k;
+    auto pad = [](int64_t b) { return (b + 255) & ~int64_t(255); };
+    Workspace w{};
+    const bool direct = slots <= kDirectSlots;
+    w.order = 0;
+    w.items = w.order + (direct ? 0 : pad(4 * slots));
+    w.nitems = w.items + (direct ? 0 : pad(12 * max_items(slots, E, block_rows(slots, E))));
+    w.h = w.nitems + (direct ? 0 : 256);
+    w.rows = w.h + pad(2 * slots * I);
+    w.bytes = w.rows + (direct ? 0 : pad(4 * slots * H));
+    return w;
+}
+
+bool experts_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+    if (!valid_mn(T) || k < 1 || k > QLIN_MAX_CHOICES || T * k > QLIN_MAX_MN) return false;
+    if (E < 1 || E > QLIN_MAX_EXPERTS || !valid_k(H) || !valid_k(I)) return false;
+    return T * k * (H > I ? H : I) <= kMaxElements;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t qlin_experts_w4_workspace(int64_t T, int32_t k, int64_t E, int64_t H, int64_t I) {
+    if (!experts_sizes(T, k, E, H, I)) return 0;
+    return layout(T, k, E, H, I).bytes;
+}
+
+qlin_status qlin_experts_w4(const uint16_t* x, int64_t T, int64_t H, int64_t I, int64_t E, int32_t k, int32_t group,
+                            const int32_t* ids, const float* weights, const qlin_w4_weight* gate,
+                            const qlin_w4_weight* up, const qlin_w4_weight* down, uint16_t* y, void* workspace,
+                            hipStream_t stream) {
+    if (!gate || !up || !down) return QLIN_ERR_NULL;
+    if (!experts_sizes(T, k, E, H, I) || !valid_group(group, H) || !valid_group(group, I)) return QLIN_ERR_SHAPE;
+    if (gate->n != I || up->n != I || down->n != H) return QLIN_ERR_SHAPE;
+    if (T == 0) return QLIN_OK;
+    if (!x || !ids || !weights || !y || !workspace) return QLIN_ERR_NULL;
+    for (const qlin_w4_weight* w : {gate, up, down}) {
+        const qlin_status st = check_pointers(*w);
+        if (st != QLIN_OK) return st;
+    }
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+        return QLIN_ERR_ALIGN;
+    const int64_t slots = T * k;
+    const Workspace l = layout(T, k, E, H, I);
+    const Range ry = rng(y, 2 * T * H), rw = rng(workspace, l.bytes);
+    if (overlap(ry, rw)) return QLIN_ERR_ALIAS;
+    for (Range written : {ry, rw}) {
+        if (overlap(written, rng(x, 2 * T * H)) || overlap(written, rng(ids, 4 * slots)) ||
+            overlap(written, rng(weights, 4 * slots)))
+            return QLIN_ERR_ALIAS;
+        if (overlap(written, ranges(*gate, E, H, group)) || overlap(written, ranges(*up, E, H, group)) ||
+            overlap(written, ranges(*down, E, I, group)))
+            return QLIN_ERR_ALIAS;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const bool direct = slots <= kDirectSlots;
+    int* order = reinterpret_cast<int*>(ws + l.order);
+    int* items = reinterpret_cast<int*>(ws + l.items);
+    int* nitems = reinterpret_cast<int*>(ws + l.nitems);
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
+    float* rows = reinterpret_cast<float*>(ws + l.rows);
+
+    qlin::W4Call c{};
+    c.group = group;
+    c.ids = ids;
+    c.E = (int)E;
+    c.block_rows = direct ? 1 : block_rows(slots, E);
+    c.max_items = direct ? slots : max_items(slots, E, c.block_rows);
+    if (!direct) {
+        const hipError_t e = qlin::launch_experts_plan(ids, slots, (int)E, c.block_rows, order, items, nitems, stream);
+        if (e != hipSuccess) return qlin::hip_status(e);
+        c.order = order;
+        c.items = items;
+        c.nitems = nitems;
+    }
+    c.x = x;
+    c.w[0] = gate->q_w, c.w[1] = up->q_w;
+    c.s[0] = gate->s_w, c.s[1] = up->s_w;
+    c.z[0] = gate->z_w, c.z[1] = up->z_w;
+    c.y[0] = h;
+    c.n[0] = c.n[1] = (int)I;
+    c.nseg = 2;
+    c.mode = QLIN_OUT_BF16;
+    c.K = H;
+    c.xdiv = k;
+    hipError_t e = qlin::launch_w4_stream(c, true, true, stream);
+    if (e != hipSuccess) return qlin::hip_status(e);
+    c.x = h;
+    c.w[0] = down->q_w;
+    c.s[0] = down->s_w;
+    c.z[0] = down->z_w;
+    c.w[1] = nullptr, c.s[1] = nullptr, c.z[1] = nullptr;
+    c.y[0] = rows;
+    c.n[0] = (int)H;
+    c.nseg = 1;
+    c.mode = QLIN_OUT_F32;
+    c.K = I;
+    c.xdiv = 1;
+    if (direct) return qlin::hip_status(qlin::launch_experts_down_direct(c, weights, T, k, y, stream));
+    e = qlin::launch_w4_stream(c, false, true, stream);
+    if (e != hipSuccess) return qlin::hip_status(e);
+    return qlin::hip_status(qlin::launch_experts_combine(rows, ids, weights, T, k, (int)E, H, y, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,71 @@
+// Launchers of the 4-bit products, the router and the experts' MLP.  All
+// arguments are validated by the caller (w4_api.hip) before a launch.
+// Host declarations only.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "../../include/qlin_w4.h"
+
+namespace qlin {
+
+// Packed 4-bit weights: one matrix [N, K] is ceil(N / 16) row tiles, each
+// ceil(K / 128) blocks of 1 KiB (16 rows x 128 inputs), see qlin_pack_w4.
+constexpr int kW4Rows = 16;
+constexpr int kW4K = 128;
+constexpr int kW4Block = 1024;
+inline int64_t w4_row_tiles(int64_t N) { return (N + kW4Rows - 1) / kW4Rows; }
+inline int64_t w4_k_tiles(int64_t K) { return (K + kW4K - 1) / kW4K; }
+
+constexpr int kW4Segments = 4;
+
+// One product launch.  Dense: up to four weight matrices reading the same M
+// rows of x.  Experts: one matrix (or a gate/up pair) per expert and the
+// routed rows of the items below.
+struct W4Call {
+    const uint16_t* x;                 // bf16 [rows, K]
+    const uint8_t* w[kW4Segments];     // packed codes (experts: [E] matrices)
+    const uint16_t* s[kW4Segments];    // bf16 scales [N, K / G]
+    const uint8_t* z[kW4Segments];     // zero points [N, K / G], or null (8)
+    void* y[kW4Segments];
+    int n[kW4Segments];                // output rows of each matrix
+    int nseg;
+    int mode;                          // OutMode of y
+    int group;                         // inputs per scale: 32, 64 or 128
+    int64_t M, K;
+    // experts
+    const int* ids;                    // expert of each slot (slot = token * k + choice)
+    const int* order;                  // slots in the order of their experts
+    const int* items;                  // {expert, first place in order, rows}; null: item i is slot i alone
+    const int* nitems;
+    int E;
+    int xdiv;                          // row of x of a slot: slot / xdiv
+    int64_t max_items;                 // bound of *nitems (slots where items is null)
+    int block_rows;                    // rows of one item at most
+};
+
+hipError_t launch_pack_w4(const uint8_t* q, int64_t E, int64_t N, int64_t K, uint8_t* p, hipStream_t st);
+
+// Rows of x that one pass of the streaming kernel takes.
+constexpr int kW4StreamMaxM = 64;
+// y (or, with pair, h = silu(x w[0]^T) * (x w[1]^T)) by the streaming kernel:
+// any M (token blocks of up to kW4StreamMaxM along the grid).
+hipError_t launch_w4_stream(const W4Call& c, bool pair, bool experts, hipStream_t st);
+
+hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int k, int score, const float* bias, int groups,
+                        int top_groups, int group_best, bool renorm, float scale, int32_t* ids, float* weights,
+                        hipStream_t st);
+
+// The routed rows sorted by expert and cut into items of at most block_rows
+// rows of one expert.  order [T * k], items [3 * max_items], nitems [1].
+hipError_t launch_experts_plan(const int32_t* ids, int64_t slots, int E, int block_rows, int* order, int* items,
+                               int* nitems, hipStream_t st);
+// y[t] = sum_j weights[t, j] * rows[t * k + j] over the slots with an expert.
+hipError_t launch_experts_combine(const float* rows, const int32_t* ids, const float* weights, int64_t T, int k, int E,
+                                  int64_t H, uint16_t* y, hipStream_t st);
+// The down projection and the weighted sum of few tokens in one launch.
+hipError_t launch_experts_down_direct(const W4Call& c, const float* weights, int64_t T, int k, uint16_t* y,
+                                      hipStream_t st);
+
+}  // namespace qlin

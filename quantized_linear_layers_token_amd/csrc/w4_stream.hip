@@ -1,0 +1,358 @@
+// Products of few rows on 4-bit weights: every weight byte is read once per
+// block of tokens, straight into the matrix-core operand registers.
+//
+//   y[m, n] = sum_g s[n, g] * ( sum_{k in g} x[m, k] * code[n, k]  -  z[n, g] * sum_{k in g} x[m, k] )
+//
+// Bound by HBM at few tokens (half a byte per weight).  One wavefront takes R
+// tiles of 16 weight rows and a share of the inputs; the NW wavefronts of a
+// workgroup split the inputs and add their partial sums through LDS in a fixed
+// order.  The packed order makes every weight load 1 KiB contiguous per
+// wavefront, and lets one 16x16x32 bf16 product take eight codes of a lane
+// after seven instructions of widening.  The matrix cores are idle otherwise,
+// so the sums of x that the zero points need are a product with a constant
+// operand: of -8 where there are no zero points, and its result is then the
+// start value of every tile's sum.  Groups are summed in f32 and scaled in f32.
+#include "w4_device.h"
+
+namespace qlin {
+
+namespace {
+
+template <int G, int MT, int R, int NW, bool ZP, bool PAIR, bool EXPERTS>
+__global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, int units, int units0, int units1, int units2) {
+    constexpr int SUB = kW4K / G;                 // groups in a 128-input block
+    constexpr int SL = G / 32;                    // 32-input slices of a group
+    constexpr int U = MT >= 4 ? 1 : (MT * R >= 2 ? 2 : 4);   // blocks of inputs in flight
+    constexpr int T = MT * 16;
+    __shared__ __attribute__((aligned(16))) float red[NW * R * T * 16];
+
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63;
+    const int q = lane >> 4, col = lane & 15;
+
+    // the matrix and its first row tile
+    const int block = (int)(blockIdx.x / (unsigned)units);   // token block or item
+    int unit = (int)(blockIdx.x % (unsigned)units), seg = 0;
+    if constexpr (!PAIR && !EXPERTS) {
+        if (unit >= units0) { unit -= units0; seg = 1; }
+        if (seg == 1 && unit >= units1) { unit -= units1; seg = 2; }
+        if (seg == 2 && unit >= units2) { unit -= units2; seg = 3; }
+    }
+    const int N = PAIR || EXPERTS ? c.n[0] : pick_int(c.n, seg);
+    const int tiles = (N + 15) >> 4;
+    const int tile0 = PAIR ? unit : unit * R;
+    const int K = (int)c.K, NG = K / G;
+
+    // the rows of x
+    int e = 0, begin = 0, rows;
+    int64_t m0 = 0;
+    if constexpr (EXPERTS) {
+        const int item = block;
+        if (c.items) {
+            if (item >= *c.nitems) return;
+            e = c.items[3 * item];
+            begin = c.items[3 * item + 1];
+            rows = c.items[3 * item + 2];
+        } else {
+            e = c.ids[item];
+            if ((unsigned)e >= (unsigned)c.E) return;
+            rows = 1;
+        }
+    } else {
+        m0 = (int64_t)block * T;
+        rows = (int)min((int64_t)T, c.M - m0);
+    }
+    auto row_of = [&](int t) -> int64_t {         // output row of the block's row t
+        if constexpr (EXPERTS) return c.items ? (int64_t)c.order[begin + t] : (int64_t)block;
+        else return m0 + t;
+    };
+    const uint16_t* xp[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int64_t r = row_of(min(mt * 16 + col, rows - 1));
+        xp[mt] = c.x + (EXPERTS ? r / c.xdiv : r) * K + q * 8;
+    }
+    const uint8_t* wp[R];
+    const uint16_t* sp[R];
+    const uint8_t* zp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int tile = PAIR ? tile0 : min(tile0 + r, tiles - 1);
+        const int m = PAIR ? r : seg;
+        const int64_t n = (int64_t)e * N + min(tile * 16 + col, N - 1);
+        wp[r] = (PAIR || EXPERTS ? c.w[PAIR ? r : 0] : pick_ptr(c.w, m)) + ((int64_t)e * tiles + tile) * KT * kW4Block + lane * 16;
+        sp[r] = (PAIR || EXPERTS ? c.s[PAIR ? r : 0] : pick_ptr(c.s, m)) + n * NG;
+        if constexpr (ZP) {
+            const uint8_t* zb = PAIR || EXPERTS ? c.z[PAIR ? r : 0] : pick_ptr(c.z, m);
+            zp[r] = zb ? zb + n * NG : nullptr;
+        }
+    }
+
+    const int per = (KT + NW - 1) / NW;
+    const int k0 = wave * per, k1 = min(KT, k0 + per);
+    const int slices = K >> 5;
+    const v8bf ones = bf16_const(ZP ? 1.0f : -8.0f);
+    v4f tot[R][MT] = {};
+
+    for (int kt = k0; kt < k1; kt += U) {
+        v4u w[U][R];
+        v8bf a[U][MT][4];
+        float s[U][R][SUB], z[U][R][SUB];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = min(kt + u, k1 - 1);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                w[u][r] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(wp[r] + (int64_t)b * kW4Block));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    a[u][mt][j] = *reinterpret_cast<const v8bf*>(xp[mt] + 32 * min(4 * b + j, slices - 1));
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int g = 0; g < SUB; ++g) {
+                    const int at = min(b * SUB + g, NG - 1);
+                    s[u][r][g] = bf16_lo(sp[r][at]);
+                    if constexpr (ZP) z[u][r][g] = zp[r] ? -(float)zp[r][at] : -8.0f;
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (kt + u >= k1) break;
+#pragma unroll
+            for (int g = 0; g < SUB; ++g) {
+                if ((kt + u) * SUB + g >= NG) break;   // inputs past K in the last block
+                v4f c0[MT] = {};
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < SL; ++j) c0[mt] = mfma_bf16(a[u][mt][g * SL + j], ones, c0[mt]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    v4f acc[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[mt] = c0[mt];
+                        if constexpr (ZP) acc[mt] *= z[u][r][g];
+                    }
+#pragma unroll
+                    for (int j = 0; j < SL; ++j) {
+                        const v8bf b = w4_codes(w[u][r][g * SL + j]);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_bf16(a[u][mt][g * SL + j], b, acc[mt]);
+                    }
+                    mfma_drain();
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tot[r][mt][i] = __builtin_fmaf(s[u][r][g], acc[mt][i], tot[r][mt][i]);
+                }
+            }
+        }
+    }
+
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = mt * 16 + 4 * q + i;
+                if (t < rows) red[(wave * R + r) * (T * 16) + t * 16 + col] = tot[r][mt][i];
+            }
+    __syncthreads();
+    auto sum = [&](int r, int at) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) v += red[(i * R + r) * (T * 16) + at];
+        return v;
+    };
+    constexpr int W = PAIR ? 16 : 16 * R;         // outputs of one row
+    for (int idx = tid; idx < rows * W; idx += NW * 64) {
+        const int t = idx / W, n = idx % W, r = PAIR ? 0 : n / 16;
+        const int nn = tile0 * 16 + n;
+        if (nn >= N) continue;
+        const int at = t * 16 + (n & 15);
+        const int64_t o = row_of(t) * N + nn;
+        if constexpr (PAIR) static_cast<uint16_t*>(c.y[0])[o] = swiglu_f32(sum(0, at), sum(1, at));
+        else store_f32(EXPERTS ? c.y[0] : pick_ptr(c.y, seg), o, sum(r, at), c.mode);
+    }
+}
+
+// The down projection of few tokens with the weighted sum over their experts:
+//   y[t, n] = sum_j weights[t, j] * sum_k h[t * k + j, k] * w[ids[t, j]][n, k].
+// A workgroup takes one token and 16 output rows; its wavefronts share out the
+// (slot, 128-input block) pairs, so that a single token still keeps every load
+// of its 16 rows in flight, and no row of a slot passes through memory.
+template <int G, int NW, bool ZP>
+__global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int KT, int units, const float* __restrict__ weights,
+                                                                 int k, uint16_t* __restrict__ y) {
+    constexpr int SUB = kW4K / G, SL = G / 32, U = 4;
+    __shared__ float red[NW * 16];
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63;
+    const int q = lane >> 4, col = lane & 15;
+    const int64_t t = blockIdx.x / (unsigned)units;
+    const int tile = (int)(blockIdx.x % (unsigned)units);
+    const int N = c.n[0], K = (int)c.K, NG = K / G, slices = K >> 5;
+    const int n = min(tile * 16 + col, N - 1);
+    const int id = lane < k ? c.ids[t * k + lane] : -1;
+    const float wt = lane < k ? weights[t * k + lane] : 0.0f;
+
+    const int all = k * KT, per = (all + NW - 1) / NW;
+    const int f0 = wave * per, f1 = min(all, f0 + per);
+    const v8bf ones = bf16_const(ZP ? 1.0f : -8.0f);
+    float tot = 0.0f;
+    for (int f = f0; f < f1; f += U) {
+        v4u w[U];
+        v8bf a[U][4];
+        float s[U][SUB], z[U][SUB], wu[U];
+        int kb[U];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = min(f + u, f1 - 1), j = at / KT;
+            kb[u] = at - j * KT;
+            const int e = __builtin_amdgcn_readlane(id, j);
+            wu[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), j));
+            live[u] = (unsigned)e < (unsigned)c.E && f + u < f1;
+            const int64_t ee = live[u] ? e : 0;    // a slot without an expert reads expert 0 and is dropped
+            w[u] = __builtin_nontemporal_load(
+                reinterpret_cast<const v4u*>(c.w[0] + ((ee * units + tile) * KT + kb[u]) * kW4Block + lane * 16));
+            const uint16_t* xr = c.x + (t * k + j) * (int64_t)K + q * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[u][i] = *reinterpret_cast<const v8bf*>(xr + 32 * min(4 * kb[u] + i, slices - 1));
+#pragma unroll
+            for (int g = 0; g < SUB; ++g) {
+                const int64_t sat = (ee * N + n) * NG + min(kb[u] * SUB + g, NG - 1);
+                s[u][g] = bf16_lo(c.s[0][sat]);
+                if constexpr (ZP) z[u][g] = -(float)c.z[0][sat];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!live[u]) continue;
+            float part = 0.0f;
+#pragma unroll
+            for (int g = 0; g < SUB; ++g) {
+                if (kb[u] * SUB + g >= NG) break;
+                v4f acc = {};
+#pragma unroll
+                for (int j = 0; j < SL; ++j) acc = mfma_bf16(a[u][g * SL + j], ones, acc);
+                if constexpr (ZP) acc *= z[u][g];
+#pragma unroll
+                for (int j = 0; j < SL; ++j) acc = mfma_bf16(a[u][g * SL + j], w4_codes(w[u][g * SL + j]), acc);
+                mfma_drain();
+                part = __builtin_fmaf(s[u][g], acc[0], part);   // every row of the operand is the token
+            }
+            tot = __builtin_fmaf(wu[u], part, tot);
+        }
+    }
+    if (q == 0) red[wave * 16 + col] = tot;
+    __syncthreads();
+    if (tid < 16 && tile * 16 + tid < N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) v += red[i * 16 + tid];
+        y[t * N + tile * 16 + tid] = f32_to_bf16(v);
+    }
+}
+
+template <int G>
+hipError_t run_down_direct(const W4Call& c, const float* weights, int64_t T, int k, uint16_t* y, hipStream_t st) {
+    constexpr int NW = 16;
+    const int KT = (int)w4_k_tiles(c.K), units = (int)w4_row_tiles(c.n[0]);
+    const unsigned grid = (unsigned)(T * units);
+    if (c.z[0]) w4_down_direct_kernel<G, NW, true><<<grid, NW * 64, 0, st>>>(c, KT, units, weights, k, y);
+    else w4_down_direct_kernel<G, NW, false><<<grid, NW * 64, 0, st>>>(c, KT, units, weights, k, y);
+    return hipGetLastError();
+}
+
+template <int G, int MT, int R, int NW, bool PAIR, bool EXPERTS>
+hipError_t run(const W4Call& c, hipStream_t st) {
+    const int KT = (int)w4_k_tiles(c.K);
+    int units[kW4Segments] = {0, 0, 0, 0}, total = 0;
+    bool zp = false;
+    const int nm = PAIR ? 2 : c.nseg;
+    for (int i = 0; i < nm; ++i) {
+        units[i] = PAIR ? (int)w4_row_tiles(c.n[0]) : (int)((w4_row_tiles(c.n[i]) + R - 1) / R);
+        if (!PAIR || i == 0) total += units[i];
+        zp |= c.z[i] != nullptr;
+    }
+    const int64_t blocks = EXPERTS ? c.max_items : (c.M + MT * 16 - 1) / (MT * 16);
+    if (blocks * total > (int64_t(1) << 32) / (NW * 64) - 1) return hipErrorInvalidValue;   // threads of one launch
+    const unsigned grid = (unsigned)(blocks * total);
+    if (zp) w4_stream_kernel<G, MT, R, NW, true, PAIR, EXPERTS><<<grid, NW * 64, 0, st>>>(c, KT, total, units[0], units[1], units[2]);
+    else w4_stream_kernel<G, MT, R, NW, false, PAIR, EXPERTS><<<grid, NW * 64, 0, st>>>(c, KT, total, units[0], units[1], units[2]);
+    return hipGetLastError();
+}
+
+template <int G, bool PAIR, bool EXPERTS>
+hipError_t by_rows(const W4Call& c, hipStream_t st) {
+    constexpr int R = PAIR ? 2 : 1;
+    const int64_t m = EXPERTS ? c.block_rows : c.M;
+    if (m <= 16) return run<G, 1, R, 8, PAIR, EXPERTS>(c, st);
+    if (m <= 32) return run<G, 2, R, 8, PAIR, EXPERTS>(c, st);
+    return run<G, 4, 2, 4, PAIR, EXPERTS>(c, st);
+}
+
+template <bool PAIR, bool EXPERTS>
+hipError_t by_group(const W4Call& c, hipStream_t st) {
+    if (c.group == 32) return by_rows<32, PAIR, EXPERTS>(c, st);
+    if (c.group == 64) return by_rows<64, PAIR, EXPERTS>(c, st);
+    return by_rows<128, PAIR, EXPERTS>(c, st);
+}
+
+// Row-major nibbles to the packed order, one thread per packed dword.
+__global__ __launch_bounds__(256) void pack_w4_kernel(const uint8_t* __restrict__ q, int64_t N, int64_t K, int tiles, int KT,
+                                                      int64_t dwords, uint32_t* __restrict__ p) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < dwords; i += (int64_t)gridDim.x * 256) {
+        const int j = (int)(i & 3), lane = (int)(i >> 2) & 63;
+        const int64_t blk = i >> 8;
+        const int kt = (int)(blk % KT);
+        const int64_t rest = blk / KT;
+        const int64_t n = (rest % tiles) * 16 + (lane & 15);
+        const int64_t k = (int64_t)kt * 128 + 32 * j + 8 * (lane >> 4);
+        uint32_t out = 0;
+        if (n < N && k < K) {   // K % 32 == 0: the eight inputs are there together
+            const uint8_t* src = q + ((rest / tiles) * N + n) * (K / 2) + k / 2;
+            uint32_t in = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) in |= (uint32_t)src[b] << (8 * b);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                out |= ((in >> (4 * b)) & 15u) << (8 * b);
+                out |= ((in >> (16 + 4 * b)) & 15u) << (8 * b + 4);
+            }
+        }
+        p[i] = out;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_pack_w4(const uint8_t* q, int64_t E, int64_t N, int64_t K, uint8_t* p, hipStream_t st) {
+    const int64_t dwords = E * w4_row_tiles(N) * w4_k_tiles(K) * (kW4Block / 4);
+    const int64_t want = (dwords + 255) / 256;
+    pack_w4_kernel<<<(unsigned)(want < 65536 ? want : 65536), 256, 0, st>>>(q, N, K, (int)w4_row_tiles(N), (int)w4_k_tiles(K),
+                                                                          dwords, reinterpret_cast<uint32_t*>(p));
+    return hipGetLastError();
+}
+
+hipError_t launch_w4_stream(const W4Call& c, bool pair, bool experts, hipStream_t st) {
+    if (pair) return experts ? by_group<true, true>(c, st) : by_group<true, false>(c, st);
+    return experts ? by_group<false, true>(c, st) : by_group<false, false>(c, st);
+}
+
+hipError_t launch_experts_down_direct(const W4Call& c, const float* weights, int64_t T, int k, uint16_t* y,
+                                      hipStream_t st) {
+    if (c.group == 32) return run_down_direct<32>(c, weights, T, k, y, st);
+    if (c.group == 64) return run_down_direct<64>(c, weights, T, k, y, st);
+    return run_down_direct<128>(c, weights, T, k, y, st);
+}
+
+}  // namespace qlin
