@@ -12,8 +12,8 @@
  *    per `group` consecutive inputs of a row (group 32, 64 or 128; K a multiple
  *    of it) and either one zero point (uint8) per scale or 8 for all of them:
  *        w[n, k] = (code[n, k] - zero[n, k / group]) * scale[n, k / group]
- *    Scales and zero points are row-major [N, K / group].  K is a multiple of
- *    32 and at most QLIN_MAX_K; N is any number up to QLIN_MAX_MN.
+ *    K is a multiple of 32 and at most QLIN_MAX_K; N is any number up to
+ *    QLIN_MAX_MN.
  *  - The activations are bf16 and not rounded (the numerics of
  *    qlin_linear_weight_only): products of inputs and codes are exact, sums are
  *    f32 per group, scaled in f32 and added in f32.
@@ -32,28 +32,34 @@ extern "C" {
 /* Layout                                                                 */
 /* ---------------------------------------------------------------------- */
 
-/* Bytes of one matrix [N, K] in the packed order: rows are padded to a
- * multiple of 16, inputs to a multiple of 128 (0 for sizes out of range). */
+/* Bytes of the codes of one matrix [N, K] in the packed order: rows are padded
+ * to a multiple of 16, inputs to a multiple of 128 (0 for sizes out of range). */
 int64_t qlin_w4_packed_bytes(int64_t N, int64_t K);
+/* Scales (and zero points) of one matrix in the packed order. */
+int64_t qlin_w4_packed_scales(int64_t N, int64_t K, int32_t group);
 
 /* E matrices of row-major codes q_w [E, N, K / 2] (byte i of a row: input 2 i
- * in the low four bits, 2 i + 1 in the high four) into the order that the
- * matrix cores read, one after the other, qlin_w4_packed_bytes(N, K) each:
- *   with T = ceil(K / 128), dword j < 4 of lane l < 64 of block (n / 16, k / 128),
- *   at byte ((n / 16) * T + k / 128) * 1024 + 16 l + 4 j, holds row
- *   n = 16 (n / 16) + l % 16, inputs 128 (k / 128) + 32 j + 8 (l / 16) + 0..7:
- *   its byte b has input b in the low four bits and input 4 + b in the high.
- * Padding is written as zeros.  q_w and q_w_packed: 16-byte aligned, not
- * overlapping.  Every call below reads this one layout, for one token as for
- * long inputs: the row-major codes need not be kept. */
-qlin_status qlin_pack_w4(const uint8_t* q_w, int64_t E, int64_t N, int64_t K, uint8_t* q_w_packed, hipStream_t stream);
+ * in the low four bits, 2 i + 1 in the high four), scales s_w and zero points
+ * z_w [E, N, K / group] (z_w null: none) into the order that the matrix cores
+ * read, one matrix after the other.  A block is 16 rows x 128 inputs; block
+ * (n / 16) * ceil(K / 128) + k / 128 of a matrix holds
+ *   codes, 1024 bytes: dword j < 4 of lane l < 64, at byte 16 l + 4 j, has row
+ *     l % 16, inputs 32 j + 8 (l / 16) + 0..7 of the block: its byte b has input b
+ *     of those in the low four bits and input 4 + b in the high four;
+ *   scales and zero points, 16 * (128 / group) entries each: row by row.
+ * Padding is written as zeros.  q_w and q_w_packed are 16-byte aligned, s_w 2,
+ * s_w_packed 8, z_w_packed 4; nothing overlaps; z_w and z_w_packed are both
+ * null or neither.  Every call below reads this one layout, for one token as
+ * for long inputs: the row-major weights need not be kept. */
+qlin_status qlin_pack_w4(const uint8_t* q_w, const uint16_t* s_w, const uint8_t* z_w, int64_t E, int64_t N, int64_t K,
+                         int32_t group, uint8_t* q_w_packed, uint16_t* s_w_packed, uint8_t* z_w_packed,
+                         hipStream_t stream);
 
-/* A packed matrix, or E of them one after the other (then s_w and z_w are
- * [E, N, K / group]).  z_w may be null: every zero point is 8. */
+/* A packed matrix, or E of them one after the other. */
 typedef struct qlin_w4_weight {
     const uint8_t* q_w;   /* packed codes, 16-byte aligned */
-    const uint16_t* s_w;  /* bf16 scales */
-    const uint8_t* z_w;   /* zero points, or null */
+    const uint16_t* s_w;  /* packed scales, 8-byte aligned */
+    const uint8_t* z_w;   /* packed zero points, 4-byte aligned, or null: every zero point is 8 */
     int64_t n;            /* rows N of each matrix */
 } qlin_w4_weight;
 

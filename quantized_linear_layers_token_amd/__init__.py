@@ -63,7 +63,8 @@ MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
 _F = ctypes.c_float
 SIGNATURES_W4 = {
     "qlin_w4_packed_bytes": (_I64, [_I64, _I64]),
-    "qlin_pack_w4": (_S, [_P, _I64, _I64, _I64, _P, _P]),
+    "qlin_w4_packed_scales": (_I64, [_I64, _I64, _I32]),
+    "qlin_pack_w4": (_S, [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _P]),
     "qlin_linear_w4": (_S, [_P, _I64, _I64, _I32, _P, _P, _I32, _S, _P]),
     "qlin_linear_swiglu_w4": (_S, [_P, _I64, _I64, _I32, _P, _P, _P, _P]),
     "qlin_route": (_S, [_P, _S, _I64, _I64, _I32, _S, _P, _I32, _I32, _I32, _I32, _F, _P, _P, _P]),
@@ -362,9 +363,8 @@ def qlin_linear_swiglu(scheme, x, gate, up, h, q_x=None, s_x=None, stream=None):
 # --------------------------------------------------------------------------
 
 class W4Weight:
-    """4-bit weights laid out for the library (qlin_pack_w4): one matrix
-    [N, K], or `experts` of them.  Holds the packed codes and the scales and
-    zero points it was made with (they are used in place)."""
+    """4-bit weights laid out for the library by qlin_pack_w4: one matrix
+    [N, K], or `experts` of them.  Owns the packed tensors."""
 
     def __init__(self, packed, scales, zeros, experts, N, K, group):
         self.packed, self.scales, self.zeros = packed, scales, zeros
@@ -405,7 +405,7 @@ def _w4_tensor(t, name, shape, size, device):
 def qlin_pack_w4(q_w, s_w, z_w=None, stream=None):
     """q_w uint8 [N, K/2] (input 2 i in the low half of byte i) or [E, N, K/2],
     s_w bf16 [.., N, K/group], z_w uint8 like s_w or None (8) -> W4Weight.
-    The packed codes are a new tensor; q_w need not be kept."""
+    The packed weights are new tensors; the arguments need not be kept."""
     import torch
     if q_w.dim() not in (2, 3) or s_w.dim() != q_w.dim():
         raise ValueError("q_w must be [N, K/2] or [E, N, K/2], s_w [N, K/group] or [E, N, K/group]")
@@ -421,9 +421,13 @@ def qlin_pack_w4(q_w, s_w, z_w=None, stream=None):
     size = _lib.qlin_w4_packed_bytes(N, K)
     if (N and not size) or E > MAX_EXPERTS:
         raise QlinError(QLIN_ERR_SHAPE, "qlin_pack_w4")
+    count = E * _lib.qlin_w4_packed_scales(N, K, group)
     packed = torch.empty((E * size,), dtype=torch.uint8, device=q_w.device)
-    _launch("qlin_pack_w4", q_w.device, stream, q_w.data_ptr(), E, N, K, packed.data_ptr())
-    return W4Weight(packed, s_w, z_w, E, N, K, group)
+    scales = torch.empty((count,), dtype=s_w.dtype, device=q_w.device)
+    zeros = None if z_w is None else torch.empty((count,), dtype=z_w.dtype, device=q_w.device)
+    _launch("qlin_pack_w4", q_w.device, stream, q_w.data_ptr(), s_w.data_ptr(), _ptr(z_w), E, N, K, group, packed.data_ptr(),
+            scales.data_ptr(), _ptr(zeros))
+    return W4Weight(packed, scales, zeros, E, N, K, group)
 
 
 def _w4_input(x, w, name):

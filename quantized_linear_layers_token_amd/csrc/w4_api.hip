@@ -29,14 +29,14 @@ struct WeightRanges {
     Range q, s, z;
 };
 WeightRanges ranges(const qlin_w4_weight& w, int64_t E, int64_t K, int32_t group) {
-    const int64_t scales = E * w.n * (K / group);
+    const int64_t scales = E * qlin_w4_packed_scales(w.n, K, group);
     return WeightRanges{rng(w.q_w, E * qlin_w4_packed_bytes(w.n, K)), rng(w.s_w, 2 * scales), rng(w.z_w, w.z_w ? scales : 0)};
 }
 bool overlap(Range a, const WeightRanges& w) { return overlap(a, w.q) || overlap(a, w.s) || overlap(a, w.z); }
 
 qlin_status check_pointers(const qlin_w4_weight& w) {
     if (!w.q_w || !w.s_w) return QLIN_ERR_NULL;
-    if (!aligned(w.q_w, 16) || !aligned(w.s_w, 2)) return QLIN_ERR_ALIGN;
+    if (!aligned(w.q_w, 16) || !aligned(w.s_w, 8) || !aligned(w.z_w, 4)) return QLIN_ERR_ALIGN;
     return QLIN_OK;
 }
 
@@ -53,13 +53,27 @@ int64_t qlin_w4_packed_bytes(int64_t N, int64_t K) {
     return qlin::w4_row_tiles(N) * qlin::w4_k_tiles(K) * qlin::kW4Block;
 }
 
-qlin_status qlin_pack_w4(const uint8_t* q_w, int64_t E, int64_t N, int64_t K, uint8_t* q_w_packed, hipStream_t stream) {
-    if (E < 0 || E > QLIN_MAX_EXPERTS || !valid_mn(N) || !valid_k(K)) return QLIN_ERR_SHAPE;
+int64_t qlin_w4_packed_scales(int64_t N, int64_t K, int32_t group) {
+    if (!valid_mn(N) || !valid_k(K) || !valid_group(group, K)) return 0;
+    return qlin::w4_row_tiles(N) * qlin::w4_k_tiles(K) * qlin::kW4Rows * (qlin::kW4K / group);
+}
+
+qlin_status qlin_pack_w4(const uint8_t* q_w, const uint16_t* s_w, const uint8_t* z_w, int64_t E, int64_t N, int64_t K,
+                         int32_t group, uint8_t* q_w_packed, uint16_t* s_w_packed, uint8_t* z_w_packed,
+                         hipStream_t stream) {
+    if (E < 0 || E > QLIN_MAX_EXPERTS || !valid_mn(N) || !valid_k(K) || !valid_group(group, K)) return QLIN_ERR_SHAPE;
     if (E == 0 || N == 0) return QLIN_OK;
-    if (!q_w || !q_w_packed) return QLIN_ERR_NULL;
-    if (!aligned(q_w, 16) || !aligned(q_w_packed, 16)) return QLIN_ERR_ALIGN;
-    if (overlap(rng(q_w, E * N * (K / 2)), rng(q_w_packed, E * qlin_w4_packed_bytes(N, K)))) return QLIN_ERR_ALIAS;
-    return qlin::hip_status(qlin::launch_pack_w4(q_w, E, N, K, q_w_packed, stream));
+    if (!q_w || !s_w || !q_w_packed || !s_w_packed || (z_w == nullptr) != (z_w_packed == nullptr)) return QLIN_ERR_NULL;
+    if (!aligned(q_w, 16) || !aligned(s_w, 2) || !aligned(q_w_packed, 16) || !aligned(s_w_packed, 8) || !aligned(z_w_packed, 4))
+        return QLIN_ERR_ALIGN;
+    const int64_t scales = E * N * (K / group), packed = E * qlin_w4_packed_scales(N, K, group);
+    const Range in[3] = {rng(q_w, E * N * (K / 2)), rng(s_w, 2 * scales), rng(z_w, z_w ? scales : 0)};
+    const Range out[3] = {rng(q_w_packed, E * qlin_w4_packed_bytes(N, K)), rng(s_w_packed, 2 * packed),
+                          rng(z_w_packed, z_w ? packed : 0)};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 3; ++j)
+            if (overlap(out[i], in[j]) || (i != j && overlap(out[i], out[j]))) return QLIN_ERR_ALIAS;
+    return qlin::hip_status(qlin::launch_pack_w4(q_w, s_w, z_w, E, N, K, group, q_w_packed, s_w_packed, z_w_packed, stream));
 }
 
 qlin_status qlin_linear_w4(const uint16_t* x, int64_t M, int64_t K, int32_t group, const qlin_w4_weight* weights,

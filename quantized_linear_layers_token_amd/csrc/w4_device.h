@@ -38,6 +38,29 @@ __device__ __forceinline__ v8bf bf16_const(float v) {
     return v8bf{h, h, h, h, h, h, h, h};
 }
 
+// The SUB = 128 / group scales (zero points) of a row in one block.
+template <int SUB>
+__device__ __forceinline__ void w4_scales(const uint16_t* p, float (&s)[SUB]) {
+    if constexpr (SUB == 1) {
+        s[0] = bf16_lo(*p);
+    } else if constexpr (SUB == 2) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+        s[0] = bf16_lo(v), s[1] = bf16_hi(v);
+    } else {
+        const v2u v = *reinterpret_cast<const v2u*>(p);
+        s[0] = bf16_lo(v.x), s[1] = bf16_hi(v.x), s[2] = bf16_lo(v.y), s[3] = bf16_hi(v.y);
+    }
+}
+template <int SUB>
+__device__ __forceinline__ void w4_minus_zeros(const uint8_t* p, float (&z)[SUB]) {
+    uint32_t v;
+    if constexpr (SUB == 1) v = *p;
+    else if constexpr (SUB == 2) v = *reinterpret_cast<const uint16_t*>(p);
+    else v = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) z[i] = -(float)((v >> (8 * i)) & 255u);
+}
+
 // silu(g) * u of the f32 sums, rounded once.
 __device__ __forceinline__ uint16_t swiglu_f32(float g, float u) { return f32_to_bf16(g / (1.0f + __expf(-g)) * u); }
 

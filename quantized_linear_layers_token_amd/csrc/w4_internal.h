@@ -26,8 +26,8 @@ constexpr int kW4Segments = 4;
 struct W4Call {
     const uint16_t* x;                 // bf16 [rows, K]
     const uint8_t* w[kW4Segments];     // packed codes (experts: [E] matrices)
-    const uint16_t* s[kW4Segments];    // bf16 scales [N, K / G]
-    const uint8_t* z[kW4Segments];     // zero points [N, K / G], or null (8)
+    const uint16_t* s[kW4Segments];    // packed scales
+    const uint8_t* z[kW4Segments];     // packed zero points, or null (8)
     void* y[kW4Segments];
     int n[kW4Segments];                // output rows of each matrix
     int nseg;
@@ -45,7 +45,8 @@ struct W4Call {
     int block_rows;                    // rows of one item at most
 };
 
-hipError_t launch_pack_w4(const uint8_t* q, int64_t E, int64_t N, int64_t K, uint8_t* p, hipStream_t st);
+hipError_t launch_pack_w4(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t E, int64_t N, int64_t K, int group,
+                          uint8_t* qp, uint16_t* sp, uint8_t* zp, hipStream_t st);
 
 // Rows of x that one pass of the streaming kernel takes.
 constexpr int kW4StreamMaxM = 64;

@@ -80,12 +80,12 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
     for (int r = 0; r < R; ++r) {
         const int tile = PAIR ? tile0 : min(tile0 + r, tiles - 1);
         const int m = PAIR ? r : seg;
-        const int64_t n = (int64_t)e * N + min(tile * 16 + col, N - 1);
-        wp[r] = (PAIR || EXPERTS ? c.w[PAIR ? r : 0] : pick_ptr(c.w, m)) + ((int64_t)e * tiles + tile) * KT * kW4Block + lane * 16;
-        sp[r] = (PAIR || EXPERTS ? c.s[PAIR ? r : 0] : pick_ptr(c.s, m)) + n * NG;
+        const int64_t at = ((int64_t)e * tiles + tile) * KT;
+        wp[r] = (PAIR || EXPERTS ? c.w[PAIR ? r : 0] : pick_ptr(c.w, m)) + at * kW4Block + lane * 16;
+        sp[r] = (PAIR || EXPERTS ? c.s[PAIR ? r : 0] : pick_ptr(c.s, m)) + (at * 16 + col) * SUB;
         if constexpr (ZP) {
             const uint8_t* zb = PAIR || EXPERTS ? c.z[PAIR ? r : 0] : pick_ptr(c.z, m);
-            zp[r] = zb ? zb + n * NG : nullptr;
+            zp[r] = zb ? zb + (at * 16 + col) * SUB : nullptr;
         }
     }
 
@@ -111,13 +111,17 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
                 for (int mt = 0; mt < MT; ++mt)
                     a[u][mt][j] = *reinterpret_cast<const v8bf*>(xp[mt] + 32 * min(4 * b + j, slices - 1));
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
+                w4_scales<SUB>(sp[r] + b * 16 * SUB, s[u][r]);
+                if constexpr (ZP) {
+                    if (zp[r]) {
+                        w4_minus_zeros<SUB>(zp[r] + b * 16 * SUB, z[u][r]);
+                    } else {
 #pragma unroll
-                for (int g = 0; g < SUB; ++g) {
-                    const int at = min(b * SUB + g, NG - 1);
-                    s[u][r][g] = bf16_lo(sp[r][at]);
-                    if constexpr (ZP) z[u][r][g] = zp[r] ? -(float)zp[r][at] : -8.0f;
+                        for (int g = 0; g < SUB; ++g) z[u][r][g] = -8.0f;
+                    }
                 }
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -144,7 +148,7 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_bf16(a[u][mt][g * SL + j], b, acc[mt]);
                     }
-                    mfma_drain();
+
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -199,7 +203,6 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
     const int64_t t = blockIdx.x / (unsigned)units;
     const int tile = (int)(blockIdx.x % (unsigned)units);
     const int N = c.n[0], K = (int)c.K, NG = K / G, slices = K >> 5;
-    const int n = min(tile * 16 + col, N - 1);
     const int id = lane < k ? c.ids[t * k + lane] : -1;
     const float wt = lane < k ? weights[t * k + lane] : 0.0f;
 
@@ -226,12 +229,9 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
             const uint16_t* xr = c.x + (t * k + j) * (int64_t)K + q * 8;
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[u][i] = *reinterpret_cast<const v8bf*>(xr + 32 * min(4 * kb[u] + i, slices - 1));
-#pragma unroll
-            for (int g = 0; g < SUB; ++g) {
-                const int64_t sat = (ee * N + n) * NG + min(kb[u] * SUB + g, NG - 1);
-                s[u][g] = bf16_lo(c.s[0][sat]);
-                if constexpr (ZP) z[u][g] = -(float)c.z[0][sat];
-            }
+            const int64_t sat = (((ee * units + tile) * KT + kb[u]) * 16 + col) * SUB;
+            w4_scales<SUB>(c.s[0] + sat, s[u]);
+            if constexpr (ZP) w4_minus_zeros<SUB>(c.z[0] + sat, z[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
                 if constexpr (ZP) acc *= z[u][g];
 #pragma unroll
                 for (int j = 0; j < SL; ++j) acc = mfma_bf16(a[u][g * SL + j], w4_codes(w[u][g * SL + j]), acc);
-                mfma_drain();
+
                 part = __builtin_fmaf(s[u][g], acc[0], part);   // every row of the operand is the token
             }
             tot = __builtin_fmaf(wu[u], part, tot);
@@ -307,16 +307,18 @@ hipError_t by_group(const W4Call& c, hipStream_t st) {
     return by_rows<128, PAIR, EXPERTS>(c, st);
 }
 
-// Row-major nibbles to the packed order, one thread per packed dword.
-__global__ __launch_bounds__(256) void pack_w4_kernel(const uint8_t* __restrict__ q, int64_t N, int64_t K, int tiles, int KT,
-                                                      int64_t dwords, uint32_t* __restrict__ p) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < dwords; i += (int64_t)gridDim.x * 256) {
+// Row-major weights to the packed order: one thread per packed dword of
+// codes, then one per scale.
+__global__ __launch_bounds__(256) void pack_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ s,
+                                                      const uint8_t* __restrict__ z, int64_t N, int64_t K, int G, int tiles,
+                                                      int KT, int64_t blocks, uint32_t* __restrict__ qp,
+                                                      uint16_t* __restrict__ sp, uint8_t* __restrict__ zp) {
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = first; i < blocks * 256; i += step) {
         const int j = (int)(i & 3), lane = (int)(i >> 2) & 63;
-        const int64_t blk = i >> 8;
-        const int kt = (int)(blk % KT);
-        const int64_t rest = blk / KT;
+        const int64_t blk = i >> 8, rest = blk / KT;
         const int64_t n = (rest % tiles) * 16 + (lane & 15);
-        const int64_t k = (int64_t)kt * 128 + 32 * j + 8 * (lane >> 4);
+        const int64_t k = (blk % KT) * 128 + 32 * j + 8 * (lane >> 4);
         uint32_t out = 0;
         if (n < N && k < K) {   // K % 32 == 0: the eight inputs are there together
             const uint8_t* src = q + ((rest / tiles) * N + n) * (K / 2) + k / 2;
@@ -329,17 +331,26 @@ __global__ __launch_bounds__(256) void pack_w4_kernel(const uint8_t* __restrict_
                 out |= ((in >> (16 + 4 * b)) & 15u) << (8 * b + 4);
             }
         }
-        p[i] = out;
+        qp[i] = out;
+    }
+    const int sub = 128 / G;
+    for (int64_t i = first; i < blocks * 16 * sub; i += step) {
+        const int64_t blk = i / (16 * sub), rest = blk / KT;
+        const int64_t n = (rest % tiles) * 16 + (i / sub) % 16, g = (blk % KT) * sub + i % sub;
+        const bool in = n < N && g < K / G;
+        const int64_t at = ((rest / tiles) * N + n) * (K / G) + g;
+        sp[i] = in ? s[at] : 0;
+        if (zp) zp[i] = in ? z[at] : 0;
     }
 }
 
 }  // namespace
 
-hipError_t launch_pack_w4(const uint8_t* q, int64_t E, int64_t N, int64_t K, uint8_t* p, hipStream_t st) {
-    const int64_t dwords = E * w4_row_tiles(N) * w4_k_tiles(K) * (kW4Block / 4);
-    const int64_t want = (dwords + 255) / 256;
-    pack_w4_kernel<<<(unsigned)(want < 65536 ? want : 65536), 256, 0, st>>>(q, N, K, (int)w4_row_tiles(N), (int)w4_k_tiles(K),
-                                                                          dwords, reinterpret_cast<uint32_t*>(p));
+hipError_t launch_pack_w4(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t E, int64_t N, int64_t K, int group,
+                          uint8_t* qp, uint16_t* sp, uint8_t* zp, hipStream_t st) {
+    const int64_t blocks = E * w4_row_tiles(N) * w4_k_tiles(K);   // one thread block per block at most
+    pack_w4_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(
+        q, s, z, N, K, group, (int)w4_row_tiles(N), (int)w4_k_tiles(K), blocks, reinterpret_cast<uint32_t*>(qp), sp, zp);
     return hipGetLastError();
 }
 

@@ -105,21 +105,27 @@ def test_swiglu(M, I, K, group, zeros):
     check_guard(raw)
 
 
-def test_packed_layout_is_the_documented_one():
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_packed_layout_is_the_documented_one(group):
     rng = np.random.default_rng(4)
-    E, N, K = 3, 37, 352
-    codes, scales, _ = R.weights(rng, (E, N), K, 32, False)
-    got = host(Q().qlin_pack_w4(dev(codes), dev(scales)).packed)
-    q = np.zeros((E, 48, 384), np.uint8)
+    E, N, K = 3, 37, 384 if group == 128 else 448 - 32 * (group == 32)
+    codes, scales, zeros = R.weights(rng, (E, N), K, group, True)
+    w = Q().qlin_pack_w4(dev(codes), dev(scales), dev(zeros))
+    KT = -(-K // 128)
+    q = np.zeros((E, 48, 128 * KT), np.uint8)
     q[:, :N, 0:K:2], q[:, :N, 1:K:2] = codes & 15, codes >> 4
-    want = np.empty((E, 3, 3, 64, 4, 4), np.uint8)   # matrix, row tile, input block, lane, dword, byte
+    want = np.empty((E, 3, KT, 64, 4, 4), np.uint8)   # matrix, row tile, input block, lane, dword, byte
     for lane in range(64):
         for j in range(4):
             for b in range(4):
                 k = 32 * j + 8 * (lane // 16) + b
-                at = q.reshape(E, 3, 16, 3, 128)[:, :, lane % 16, :, :]
+                at = q.reshape(E, 3, 16, KT, 128)[:, :, lane % 16, :, :]
                 want[:, :, :, lane, j, b] = at[..., k] | (at[..., k + 4] << 4)
-    assert np.array_equal(got, want.reshape(-1))
+    assert np.array_equal(host(w.packed), want.reshape(-1))
+    for got, rows in ((host(w.scales).view(np.uint16), scales), (host(w.zeros), zeros)):
+        pad = np.zeros((E, 48, KT * (128 // group)), rows.dtype)
+        pad[:, :N, :K // group] = rows
+        assert np.array_equal(got, pad.reshape(E, 3, 16, KT, -1).transpose(0, 1, 3, 2, 4).reshape(-1))
 
 
 def test_mixed_zero_points_in_one_call():
