@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libqlin.so")
 ARCH = "gfx950"
 SOURCES = ["quant_act.hip", "gemv.hip", "gemm_small.hip", "gemm_large.hip", "gemm_packed.hip", "linear.hip", "linear_tokens.hip", "weight_only.hip",
            "noalloc.hip",
-           "qlin_api.hip", "w4_stream.hip", "route.hip", "experts.hip", "w4_api.hip"]
+           "qlin_api.hip", "w4_stream.hip", "w4_tiled.hip", "route.hip", "experts.hip", "w4_api.hip"]
 HEADERS = ["qlin_device.h", "qlin_internal.h", "qlin_round.h", "qlin_rows.h", "w4_device.h", "w4_internal.h"]
 
 # Never fast-math, never flush denormals: the quantizers are bit-exact against

@@ -3,6 +3,9 @@
 // runs before the first launch.
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "../../include/qlin_w4.h"
 #include "qlin_internal.h"
 #include "w4_internal.h"
@@ -43,6 +46,62 @@ qlin_status check_pointers(const qlin_w4_weight& w) {
 // Outputs and inputs of one call stay within what an address space holds, so
 // that no size computed from them overflows.
 constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+// Choice of a product's form: the one with the least estimated time, from the
+// number w of workgroups per CU.  {first, more}: us per 4096 inputs of one
+// workgroup on every CU, and of each further one, measured at 1488 x 2048,
+// 4096 x 4096, 14336 x 4096 and 4096 x 14336 with 1 to 2048 rows (group 128
+// without zero points, group 32 with them; 64 lies between).  The streaming
+// forms' workgroups share a CU (a second one costs half of the first at
+// least); the tiled forms run one (64 x 8) or two (64 x 16) at a time.
+// Examples of both sides, us: 4096 x 4096, 64 rows: 19.6, 12.5, 9.7, 9.7, 13.4,
+// 29.1, 47.3 in the order of the forms, 16 x 4 chosen; 512 rows: 125, 72, 48,
+// 46, 40, 31.6, 47.6, 64 x 8 chosen; 2048 rows: 489, 268, 179, 181, 145, 117,
+// 73.6, 64 x 16 chosen.
+struct FormCost {
+    double first, more;
+};
+constexpr FormCost kCost128[qlin::kW4Forms] = {{4.0, 3.8}, {4.5, 4.5}, {6.0, 5.8}, {6.5, 5.6}, {10.2, 10.2}, {27, 29}, {44, 68}};
+constexpr FormCost kCost32[qlin::kW4Forms] = {{5.0, 4.6}, {6.5, 6.6}, {8.0, 8.5}, {11, 7.7}, {12.5, 13}, {46, 37}, {95, 128}};
+
+double form_cost(int form, const qlin::W4Call& c, bool pair, int64_t blocks) {
+    const double w = (double)(blocks * qlin::w4_units(form, c, pair)) / 256.0;
+    FormCost f = kCost128[form];
+    const FormCost g = kCost32[form];
+    if (c.group == 32) f = g;
+    if (c.group == 64) f = FormCost{(f.first + g.first) / 2, (f.more + g.more) / 2};
+    if (w <= 1.0) return f.first;
+    if (form == qlin::kW4Tiled64x8) return std::ceil(w) * f.more;
+    if (form == qlin::kW4Tiled64x16) {           // pairs, and what is left after them
+        const double pairs = std::floor(w / 2), rest = w - 2 * pairs;
+        return pairs * f.more + (rest > 1.0 ? f.more : rest > 0.0 ? f.first : 0.0);
+    }
+    return std::max(1.5 * f.first, w * f.more);
+}
+// The grid of one launch holds fewer than 2^32 threads.
+bool form_fits(int form, const qlin::W4Call& c, bool pair, int64_t blocks) {
+    return blocks * qlin::w4_units(form, c, pair) < (int64_t(1) << 32) / qlin::kW4FormThreads[form];
+}
+// The cheapest form for items (token blocks) of `rows` rows of x at most, or any where rows is 0; -1: none fits.
+int choose_form(const qlin::W4Call& c, bool pair, bool experts, int rows) {
+    int best = -1;
+    double least = 0;
+    for (int f = pair ? 1 : 0; f < qlin::kW4Forms; ++f) {
+        if (rows && qlin::kW4FormRows[f] != rows) continue;
+        const int64_t blocks = qlin::w4_blocks(f, c, experts);
+        if (!form_fits(f, c, pair, blocks)) continue;
+        const double cost = form_cost(f, c, pair, blocks);
+        if (best < 0 || cost < least) {
+            best = f;
+            least = cost;
+        }
+    }
+    return best;
+}
+hipError_t product(int form, const qlin::W4Call& c, bool pair, bool experts, hipStream_t st) {
+    return form >= qlin::kW4Tiled64x8 ? qlin::launch_w4_tiled(form, c, pair, experts, st)
+                                      : qlin::launch_w4_stream(form, c, pair, experts, st);
+}
 
 }  // namespace
 
@@ -119,7 +178,9 @@ qlin_status qlin_linear_w4(const uint16_t* x, int64_t M, int64_t K, int32_t grou
         c.n[c.nseg] = (int)weights[i].n;
         ++c.nseg;
     }
-    return qlin::hip_status(qlin::launch_w4_stream(c, false, false, stream));
+    const int form = choose_form(c, false, false, 0);
+    if (form < 0) return QLIN_ERR_SHAPE;
+    return qlin::hip_status(product(form, c, false, false, stream));
 }
 
 qlin_status qlin_linear_swiglu_w4(const uint16_t* x, int64_t M, int64_t K, int32_t group, const qlin_w4_weight* gate,
@@ -150,7 +211,9 @@ qlin_status qlin_linear_swiglu_w4(const uint16_t* x, int64_t M, int64_t K, int32
     c.group = group;
     c.M = M;
     c.K = K;
-    return qlin::hip_status(qlin::launch_w4_stream(c, true, false, stream));
+    const int form = choose_form(c, true, false, 0);
+    if (form < 0) return QLIN_ERR_SHAPE;
+    return qlin::hip_status(product(form, c, true, false, stream));
 }
 
 qlin_status qlin_route(const void* logits, qlin_out logits_type, int64_t T, int64_t E, int32_t k, qlin_score score,
@@ -182,10 +245,7 @@ struct Workspace {
 };
 constexpr int64_t kDirectSlots = 32;     // routed rows that are multiplied one by one, without sorting
 
-int block_rows(int64_t slots, int64_t E) {
-    const int64_t per = slots / E;       // rows of an expert, if they are spread evenly
-    return per <= 8 ? 16 : per <= 24 ? 32 : 64;
-}
+// Items of at most `rows` rows that the routed rows of E experts can need.
 int64_t max_items(int64_t slots, int64_t E, int rows) { return (slots < E ? slots : E) + slots / rows; }
 
 Workspace layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
@@ -195,7 +255,7 @@ Workspace layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     const bool direct = slots <= kDirectSlots;
     w.order = 0;
     w.items = w.order + (direct ? 0 : pad(4 * slots));
-    w.nitems = w.items + (direct ? 0 : pad(12 * max_items(slots, E, block_rows(slots, E))));
+    w.nitems = w.items + (direct ? 0 : pad(12 * max_items(slots, E, 16)));
     w.h = w.nitems + (direct ? 0 : 256);
     w.rows = w.h + pad(2 * slots * I);
     w.bytes = w.rows + (direct ? 0 : pad(4 * slots * H));
@@ -252,46 +312,60 @@ qlin_status qlin_experts_w4(const uint16_t* x, int64_t T, int64_t H, int64_t I, 
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
     float* rows = reinterpret_cast<float*>(ws + l.rows);
 
-    qlin::W4Call c{};
-    c.group = group;
-    c.ids = ids;
-    c.E = (int)E;
-    c.block_rows = direct ? 1 : block_rows(slots, E);
-    c.max_items = direct ? slots : max_items(slots, E, c.block_rows);
-    if (!direct) {
-        const hipError_t e = qlin::launch_experts_plan(ids, slots, (int)E, c.block_rows, order, items, nitems, stream);
+    // gate and up, then down
+    qlin::W4Call a{}, b{};
+    a.group = b.group = group;
+    a.ids = b.ids = ids;
+    a.E = b.E = (int)E;
+    a.x = x;
+    a.w[0] = gate->q_w, a.w[1] = up->q_w;
+    a.s[0] = gate->s_w, a.s[1] = up->s_w;
+    a.z[0] = gate->z_w, a.z[1] = up->z_w;
+    a.y[0] = h;
+    a.n[0] = a.n[1] = (int)I;
+    a.nseg = 2;
+    a.mode = QLIN_OUT_BF16;
+    a.K = H;
+    a.xdiv = k;
+    b.x = h;
+    b.w[0] = down->q_w;
+    b.s[0] = down->s_w;
+    b.z[0] = down->z_w;
+    b.y[0] = rows;
+    b.n[0] = (int)H;
+    b.nseg = 1;
+    b.mode = QLIN_OUT_F32;
+    b.K = I;
+    b.xdiv = 1;
+    if (direct) {
+        a.max_items = b.max_items = slots;
+        const hipError_t e = product(choose_form(a, true, true, 16), a, true, true, stream);
         if (e != hipSuccess) return qlin::hip_status(e);
-        c.order = order;
-        c.items = items;
-        c.nitems = nitems;
+        return qlin::hip_status(qlin::launch_experts_down_direct(b, weights, T, k, y, stream));
     }
-    c.x = x;
-    c.w[0] = gate->q_w, c.w[1] = up->q_w;
-    c.s[0] = gate->s_w, c.s[1] = up->s_w;
-    c.z[0] = gate->z_w, c.z[1] = up->z_w;
-    c.y[0] = h;
-    c.n[0] = c.n[1] = (int)I;
-    c.nseg = 2;
-    c.mode = QLIN_OUT_BF16;
-    c.K = H;
-    c.xdiv = k;
-    hipError_t e = qlin::launch_w4_stream(c, true, true, stream);
-    if (e != hipSuccess) return qlin::hip_status(e);
-    c.x = h;
-    c.w[0] = down->q_w;
-    c.s[0] = down->s_w;
-    c.z[0] = down->z_w;
-    c.w[1] = nullptr, c.s[1] = nullptr, c.z[1] = nullptr;
-    c.y[0] = rows;
-    c.n[0] = (int)H;
-    c.nseg = 1;
-    c.mode = QLIN_OUT_F32;
-    c.K = I;
-    c.xdiv = 1;
-    if (direct) return qlin::hip_status(qlin::launch_experts_down_direct(c, weights, T, k, y, stream));
-    e = qlin::launch_w4_stream(c, false, true, stream);
-    if (e != hipSuccess) return qlin::hip_status(e);
-    return qlin::hip_status(qlin::launch_experts_combine(rows, ids, weights, T, k, (int)E, H, y, stream));
+    // the rows of an item: those of the cheapest pair of forms
+    int form_a = -1, form_b = -1, item_rows = 0;
+    double least = 0;
+    for (int r = 16; r <= 64; r *= 2) {
+        a.max_items = b.max_items = max_items(slots, E, r);
+        const int fa = choose_form(a, true, true, r), fb = choose_form(b, false, true, r);
+        if (fa < 0 || fb < 0) continue;
+        const double cost = form_cost(fa, a, true, a.max_items) * (double)H + form_cost(fb, b, false, b.max_items) * (double)I;
+        if (item_rows == 0 || cost < least) {
+            form_a = fa, form_b = fb, item_rows = r;
+            least = cost;
+        }
+    }
+    if (item_rows == 0) return QLIN_ERR_SHAPE;
+    a.max_items = b.max_items = max_items(slots, E, item_rows);
+    a.order = b.order = order;
+    a.items = b.items = items;
+    a.nitems = b.nitems = nitems;
+    hipError_t e = qlin::launch_experts_plan(ids, slots, (int)E, item_rows, order, items, nitems, stream);
+    if (e == hipSuccess) e = product(form_a, a, true, true, stream);
+    if (e == hipSuccess) e = product(form_b, b, false, true, stream);
+    if (e == hipSuccess) e = qlin::launch_experts_combine(rows, ids, weights, T, k, (int)E, H, y, stream);
+    return qlin::hip_status(e);
 }
 
 }  // extern "C"

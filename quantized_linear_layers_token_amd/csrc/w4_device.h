@@ -9,6 +9,10 @@ namespace qlin {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
+// A pointer to global memory: loads through it stay global loads where the
+// compiler cannot see where a pointer comes from.
+template <class T> using Global = const __attribute__((address_space(1))) T*;
+
 // Eight codes of a packed dword as bf16, in the order of their inputs: byte b
 // holds input b in its low half and input 4 + b in its high half.  A byte
 // 0x00..0x0F read as E4M3 is code * 2^-9 (subnormals below 8, the first
@@ -38,27 +42,49 @@ __device__ __forceinline__ v8bf bf16_const(float v) {
     return v8bf{h, h, h, h, h, h, h, h};
 }
 
-// The SUB = 128 / group scales (zero points) of a row in one block.
+// The SUB = 128 / group scales of a row in one block, as they are packed.
 template <int SUB>
-__device__ __forceinline__ void w4_scales(const uint16_t* p, float (&s)[SUB]) {
-    if constexpr (SUB == 1) {
-        s[0] = bf16_lo(*p);
-    } else if constexpr (SUB == 2) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-        s[0] = bf16_lo(v), s[1] = bf16_hi(v);
-    } else {
-        const v2u v = *reinterpret_cast<const v2u*>(p);
-        s[0] = bf16_lo(v.x), s[1] = bf16_hi(v.x), s[2] = bf16_lo(v.y), s[3] = bf16_hi(v.y);
+struct W4Scales {
+    uint32_t v[SUB == 4 ? 2 : 1];
+    __device__ __forceinline__ void load(Global<uint16_t> p) {
+        if constexpr (SUB == 1) {
+            v[0] = *p;
+        } else if constexpr (SUB == 2) {
+            v[0] = *(Global<uint32_t>)p;
+        } else {
+            const v2u t = *(Global<v2u>)p;
+            v[0] = t.x, v[1] = t.y;
+        }
     }
-}
+    // the same through a descriptor (a buffer load: no address registers)
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, int lane_at, int block_at) {
+        if constexpr (SUB == 1) {
+            v[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(d, lane_at, block_at, 0);
+        } else if constexpr (SUB == 2) {
+            v[0] = __builtin_amdgcn_raw_buffer_load_b32(d, lane_at, block_at, 0);
+        } else {
+            const v2u t = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(d, lane_at, block_at, 0));
+            v[0] = t.x, v[1] = t.y;
+        }
+    }
+    __device__ __forceinline__ float at(int g) const {
+        if constexpr (SUB == 1) return bf16_lo(v[0]);
+        else return g & 1 ? bf16_hi(v[g >> 1]) : bf16_lo(v[g >> 1]);
+    }
+};
+// The zero points of a row in one block: that of group g in byte g.
 template <int SUB>
-__device__ __forceinline__ void w4_minus_zeros(const uint8_t* p, float (&z)[SUB]) {
-    uint32_t v;
-    if constexpr (SUB == 1) v = *p;
-    else if constexpr (SUB == 2) v = *reinterpret_cast<const uint16_t*>(p);
-    else v = *reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-    for (int i = 0; i < SUB; ++i) z[i] = -(float)((v >> (8 * i)) & 255u);
+__device__ __forceinline__ uint32_t w4_zeros(Global<uint8_t> p) {
+    if constexpr (SUB == 1) return *p;
+    else if constexpr (SUB == 2) return *(Global<uint16_t>)p;
+    else return *(Global<uint32_t>)p;
+}
+
+template <int SUB>
+__device__ __forceinline__ uint32_t w4_zeros(__amdgpu_buffer_rsrc_t d, int lane_at, int block_at) {
+    if constexpr (SUB == 1) return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(d, lane_at, block_at, 0);
+    else if constexpr (SUB == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(d, lane_at, block_at, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b32(d, lane_at, block_at, 0);
 }
 
 // silu(g) * u of the f32 sums, rounded once.

@@ -42,17 +42,35 @@ struct W4Call {
     int E;
     int xdiv;                          // row of x of a slot: slot / xdiv
     int64_t max_items;                 // bound of *nitems (slots where items is null)
-    int block_rows;                    // rows of one item at most
 };
 
 hipError_t launch_pack_w4(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t E, int64_t N, int64_t K, int group,
                           uint8_t* qp, uint16_t* sp, uint8_t* zp, hipStream_t st);
 
-// Rows of x that one pass of the streaming kernel takes.
-constexpr int kW4StreamMaxM = 64;
-// y (or, with pair, h = silu(x w[0]^T) * (x w[1]^T)) by the streaming kernel:
-// any M (token blocks of up to kW4StreamMaxM along the grid).
-hipError_t launch_w4_stream(const W4Call& c, bool pair, bool experts, hipStream_t st);
+// Forms of a product, by the part of the output that a workgroup takes: rows
+// of x (of one expert) times row tiles of 16 weight rows.  The first five
+// stream the weights (w4_stream.hip: its eight, or four, wavefronts split the
+// inputs), the last two tile (w4_tiled.hip).  In gate/up pairs half of the row
+// tiles are the gate's, so the first is for single matrices only.
+enum W4Form : int { kW4Stream16x1 = 0, kW4Stream16x2, kW4Stream16x4, kW4Stream16x4W4, kW4Stream32x4, kW4Tiled64x8, kW4Tiled64x16, kW4Forms };
+constexpr int kW4FormRows[kW4Forms] = {16, 16, 16, 16, 32, 64, 64};
+constexpr int kW4FormTiles[kW4Forms] = {1, 2, 4, 4, 4, 8, 16};
+constexpr int kW4FormThreads[kW4Forms] = {512, 512, 512, 256, 512, 512, 256};
+
+// y (or, with pair, h = silu(x w[0]^T) * (x w[1]^T)) in the given form.
+hipError_t launch_w4_stream(int form, const W4Call& c, bool pair, bool experts, hipStream_t st);
+hipError_t launch_w4_tiled(int form, const W4Call& c, bool pair, bool experts, hipStream_t st);
+
+// Workgroups of a launch: token blocks (items) times parts of the row tiles.
+inline int64_t w4_units(int form, const W4Call& c, bool pair) {
+    const int per = kW4FormTiles[form] / (pair ? 2 : 1);
+    int64_t u = 0;
+    for (int i = 0; i < (pair ? 1 : c.nseg); ++i) u += (w4_row_tiles(c.n[i]) + per - 1) / per;
+    return u;
+}
+inline int64_t w4_blocks(int form, const W4Call& c, bool experts) {
+    return experts ? c.max_items : (c.M + kW4FormRows[form] - 1) / kW4FormRows[form];
+}
 
 hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int k, int score, const float* bias, int groups,
                         int top_groups, int group_best, bool renorm, float scale, int32_t* ids, float* weights,

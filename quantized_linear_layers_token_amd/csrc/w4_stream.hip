@@ -18,12 +18,15 @@ namespace qlin {
 
 namespace {
 
-template <int G, int MT, int R, int NW, bool ZP, bool PAIR, bool EXPERTS>
+constexpr int kAux = 2;   // buffer-load cache policy: streaming
+
+// D: blocks of 128 inputs whose loads are in flight per wavefront.
+template <int G, int MT, int R, int NW, int D, bool ZP, bool PAIR, bool EXPERTS>
 __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, int units, int units0, int units1, int units2) {
     constexpr int SUB = kW4K / G;                 // groups in a 128-input block
     constexpr int SL = G / 32;                    // 32-input slices of a group
-    constexpr int U = MT >= 4 ? 1 : (MT * R >= 2 ? 2 : 4);   // blocks of inputs in flight
     constexpr int T = MT * 16;
+    constexpr int RM = PAIR ? R / 2 : R;          // row tiles of each matrix
     __shared__ __attribute__((aligned(16))) float red[NW * R * T * 16];
 
     const int tid = threadIdx.x;
@@ -41,21 +44,20 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
     }
     const int N = PAIR || EXPERTS ? c.n[0] : pick_int(c.n, seg);
     const int tiles = (N + 15) >> 4;
-    const int tile0 = PAIR ? unit : unit * R;
-    const int K = (int)c.K, NG = K / G;
+    const int tile0 = unit * RM;
+    const int K = (int)c.K;
 
     // the rows of x
     int e = 0, begin = 0, rows;
     int64_t m0 = 0;
     if constexpr (EXPERTS) {
-        const int item = block;
         if (c.items) {
-            if (item >= *c.nitems) return;
-            e = c.items[3 * item];
-            begin = c.items[3 * item + 1];
-            rows = c.items[3 * item + 2];
+            if (block >= *c.nitems) return;
+            e = c.items[3 * block];
+            begin = c.items[3 * block + 1];
+            rows = c.items[3 * block + 2];
         } else {
-            e = c.ids[item];
+            e = c.ids[block];
             if ((unsigned)e >= (unsigned)c.E) return;
             rows = 1;
         }
@@ -67,96 +69,105 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
         if constexpr (EXPERTS) return c.items ? (int64_t)c.order[begin + t] : (int64_t)block;
         else return m0 + t;
     };
-    const uint16_t* xp[MT];
+    Global<uint16_t> xp[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int64_t r = row_of(min(mt * 16 + col, rows - 1));
-        xp[mt] = c.x + (EXPERTS ? r / c.xdiv : r) * K + q * 8;
+        xp[mt] = (Global<uint16_t>)c.x + (EXPERTS ? r / c.xdiv : r) * K + q * 8;
     }
-    const uint8_t* wp[R];
-    const uint16_t* sp[R];
-    const uint8_t* zp[R];
+
+    // this wavefront's share of the inputs: n blocks from k0.  Descriptors that
+    // cover just those: blocks past them read as zeros, codes and scales.
+    const int per = (KT + NW - 1) / NW;
+    const int k0 = min(wave * per, KT), n = min(per, KT - k0);
+    __amdgpu_buffer_rsrc_t dw[R], ds[R], dz[R];
+    bool has_z[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int tile = PAIR ? tile0 : min(tile0 + r, tiles - 1);
-        const int m = PAIR ? r : seg;
-        const int64_t at = ((int64_t)e * tiles + tile) * KT;
-        wp[r] = (PAIR || EXPERTS ? c.w[PAIR ? r : 0] : pick_ptr(c.w, m)) + at * kW4Block + lane * 16;
-        sp[r] = (PAIR || EXPERTS ? c.s[PAIR ? r : 0] : pick_ptr(c.s, m)) + (at * 16 + col) * SUB;
+        const int m = PAIR ? r / RM : seg, tile = min(tile0 + r % RM, tiles - 1);
+        const int64_t at = ((int64_t)e * tiles + tile) * KT + k0;
+        dw[r] = uniform_rsrc(pick_ptr(c.w, m) + at * kW4Block, n * kW4Block);
+        ds[r] = uniform_rsrc(pick_ptr(c.s, m) + at * 16 * SUB, n * 32 * SUB);
         if constexpr (ZP) {
-            const uint8_t* zb = PAIR || EXPERTS ? c.z[PAIR ? r : 0] : pick_ptr(c.z, m);
-            zp[r] = zb ? zb + (at * 16 + col) * SUB : nullptr;
+            const uint8_t* z = pick_ptr(c.z, m);
+            has_z[r] = z != nullptr;
+            dz[r] = uniform_rsrc(z + (has_z[r] ? at * 16 * SUB : 0), has_z[r] ? n * 16 * SUB : 0);
         }
     }
-
-    const int per = (KT + NW - 1) / NW;
-    const int k0 = wave * per, k1 = min(KT, k0 + per);
-    const int slices = K >> 5;
-    const v8bf ones = bf16_const(ZP ? 1.0f : -8.0f);
+    const int last = K / 32 - 1;                  // the last slice of 32 inputs
+    const v8bf ones = bf16_const(ZP ? -1.0f : -8.0f);
     v4f tot[R][MT] = {};
 
-    for (int kt = k0; kt < k1; kt += U) {
-        v4u w[U][R];
-        v8bf a[U][MT][4];
-        float s[U][R][SUB], z[U][R][SUB];
+    v4u w[D][R];
+    v8bf a[D][MT][4];
+    W4Scales<SUB> s[D][R];
+    uint32_t z[D][R];
+    auto load = [&](int d, int i) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int b = min(kt + u, k1 - 1);
+        for (int r = 0; r < R; ++r) {
+            w[d][r] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(dw[r], i * kW4Block + lane * 16, 0, kAux));
+            s[d][r].load(ds[r], (i * 16 + col) * 2 * SUB, 0);
+            if constexpr (ZP) z[d][r] = has_z[r] ? w4_zeros<SUB>(dz[r], (i * 16 + col) * SUB, 0) : 0x08080808u;
+        }
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                w[u][r] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(wp[r] + (int64_t)b * kW4Block));
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int mt = 0; mt < MT; ++mt) a[d][mt][j] = *(Global<v8bf>)(xp[mt] + 32 * min(4 * (k0 + i) + j, last));
+    };
+    auto multiply = [&](int d) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    a[u][mt][j] = *reinterpret_cast<const v8bf*>(xp[mt] + 32 * min(4 * b + j, slices - 1));
+        for (int g = 0; g < SUB; ++g) {           // (groups past K have scales of zero)
+            v4f c0[MT] = {};
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < SL; ++j) c0[mt] = mfma_bf16(a[d][mt][g * SL + j], ones, c0[mt]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                w4_scales<SUB>(sp[r] + b * 16 * SUB, s[u][r]);
-                if constexpr (ZP) {
-                    if (zp[r]) {
-                        w4_minus_zeros<SUB>(zp[r] + b * 16 * SUB, z[u][r]);
-                    } else {
+                v4f acc[MT];
 #pragma unroll
-                        for (int g = 0; g < SUB; ++g) z[u][r][g] = -8.0f;
+                for (int mt = 0; mt < MT; ++mt) {
+                    acc[mt] = c0[mt];
+                    if constexpr (ZP) {
+                        const float zf = (float)((z[d][r] >> (8 * g)) & 255u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[mt][i] *= zf;
                     }
                 }
-            }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (kt + u >= k1) break;
+                for (int j = 0; j < SL; ++j) {
+                    const v8bf b = w4_codes(w[d][r][g * SL + j]);
 #pragma unroll
-            for (int g = 0; g < SUB; ++g) {
-                if ((kt + u) * SUB + g >= NG) break;   // inputs past K in the last block
-                v4f c0[MT] = {};
+                    for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_bf16(a[d][mt][g * SL + j], b, acc[mt]);
+                }
+                const float sf = s[d][r].at(g);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int j = 0; j < SL; ++j) c0[mt] = mfma_bf16(a[u][mt][g * SL + j], ones, c0[mt]);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    v4f acc[MT];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        acc[mt] = c0[mt];
-                        if constexpr (ZP) acc[mt] *= z[u][r][g];
-                    }
-#pragma unroll
-                    for (int j = 0; j < SL; ++j) {
-                        const v8bf b = w4_codes(w[u][r][g * SL + j]);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_bf16(a[u][mt][g * SL + j], b, acc[mt]);
-                    }
-
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) tot[r][mt][i] = __builtin_fmaf(s[u][r][g], acc[mt][i], tot[r][mt][i]);
-                }
+                    for (int i = 0; i < 4; ++i) tot[r][mt][i] = __builtin_fmaf(sf, acc[mt][i], tot[r][mt][i]);
             }
         }
+    };
+    // one loop exit: with one after every block the compiler waits for every
+    // load in flight at the top of the loop
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        load(d, d);
+        __builtin_amdgcn_sched_barrier(0);
     }
+    int i = 0;
+    for (; i + D < n; i += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            multiply(d);
+            __builtin_amdgcn_sched_barrier(0);
+            load(d, i + D + d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (i + d < n) multiply(d);
 
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -174,14 +185,14 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
         for (int i = 0; i < NW; ++i) v += red[(i * R + r) * (T * 16) + at];
         return v;
     };
-    constexpr int W = PAIR ? 16 : 16 * R;         // outputs of one row
+    constexpr int W = 16 * RM;                    // outputs of one row
     for (int idx = tid; idx < rows * W; idx += NW * 64) {
-        const int t = idx / W, n = idx % W, r = PAIR ? 0 : n / 16;
+        const int t = idx / W, n = idx % W, r = n / 16;
         const int nn = tile0 * 16 + n;
         if (nn >= N) continue;
         const int at = t * 16 + (n & 15);
         const int64_t o = row_of(t) * N + nn;
-        if constexpr (PAIR) static_cast<uint16_t*>(c.y[0])[o] = swiglu_f32(sum(0, at), sum(1, at));
+        if constexpr (PAIR) static_cast<uint16_t*>(c.y[0])[o] = swiglu_f32(sum(r, at), sum(r + RM, at));
         else store_f32(EXPERTS ? c.y[0] : pick_ptr(c.y, seg), o, sum(r, at), c.mode);
     }
 }
@@ -208,12 +219,14 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
 
     const int all = k * KT, per = (all + NW - 1) / NW;
     const int f0 = wave * per, f1 = min(all, f0 + per);
-    const v8bf ones = bf16_const(ZP ? 1.0f : -8.0f);
+    const v8bf ones = bf16_const(ZP ? -1.0f : -8.0f);
     float tot = 0.0f;
     for (int f = f0; f < f1; f += U) {
         v4u w[U];
         v8bf a[U][4];
-        float s[U][SUB], z[U][SUB], wu[U];
+        W4Scales<SUB> s[U];
+        uint32_t z[U];
+        float wu[U];
         int kb[U];
         bool live[U];
 #pragma unroll
@@ -230,8 +243,8 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[u][i] = *reinterpret_cast<const v8bf*>(xr + 32 * min(4 * kb[u] + i, slices - 1));
             const int64_t sat = (((ee * units + tile) * KT + kb[u]) * 16 + col) * SUB;
-            w4_scales<SUB>(c.s[0] + sat, s[u]);
-            if constexpr (ZP) w4_minus_zeros<SUB>(c.z[0] + sat, z[u]);
+            s[u].load((Global<uint16_t>)c.s[0] + sat);
+            if constexpr (ZP) z[u] = w4_zeros<SUB>((Global<uint8_t>)c.z[0] + sat);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -243,11 +256,11 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
                 v4f acc = {};
 #pragma unroll
                 for (int j = 0; j < SL; ++j) acc = mfma_bf16(a[u][g * SL + j], ones, acc);
-                if constexpr (ZP) acc *= z[u][g];
+                if constexpr (ZP) acc *= (float)((z[u] >> (8 * g)) & 255u);
 #pragma unroll
                 for (int j = 0; j < SL; ++j) acc = mfma_bf16(a[u][g * SL + j], w4_codes(w[u][g * SL + j]), acc);
 
-                part = __builtin_fmaf(s[u][g], acc[0], part);   // every row of the operand is the token
+                part = __builtin_fmaf(s[u].at(g), acc[0], part);   // every row of the operand is the token
             }
             tot = __builtin_fmaf(wu[u], part, tot);
         }
@@ -272,39 +285,42 @@ hipError_t run_down_direct(const W4Call& c, const float* weights, int64_t T, int
     return hipGetLastError();
 }
 
-template <int G, int MT, int R, int NW, bool PAIR, bool EXPERTS>
+template <int G, int FORM, int NW, int D, bool PAIR, bool EXPERTS>
 hipError_t run(const W4Call& c, hipStream_t st) {
+    constexpr int MT = kW4FormRows[FORM] / 16, R = kW4FormTiles[FORM], RM = PAIR ? R / 2 : R;
+    static_assert(NW * 64 == kW4FormThreads[FORM], "threads of the form");
     const int KT = (int)w4_k_tiles(c.K);
-    int units[kW4Segments] = {0, 0, 0, 0}, total = 0;
+    const int64_t units = w4_units(FORM, c, PAIR);
+    int u[kW4Segments] = {0, 0, 0, 0};
     bool zp = false;
-    const int nm = PAIR ? 2 : c.nseg;
-    for (int i = 0; i < nm; ++i) {
-        units[i] = PAIR ? (int)w4_row_tiles(c.n[0]) : (int)((w4_row_tiles(c.n[i]) + R - 1) / R);
-        if (!PAIR || i == 0) total += units[i];
+    for (int i = 0; i < c.nseg; ++i) {
+        u[i] = (int)((w4_row_tiles(c.n[i]) + RM - 1) / RM);
         zp |= c.z[i] != nullptr;
     }
-    const int64_t blocks = EXPERTS ? c.max_items : (c.M + MT * 16 - 1) / (MT * 16);
-    if (blocks * total > (int64_t(1) << 32) / (NW * 64) - 1) return hipErrorInvalidValue;   // threads of one launch
-    const unsigned grid = (unsigned)(blocks * total);
-    if (zp) w4_stream_kernel<G, MT, R, NW, true, PAIR, EXPERTS><<<grid, NW * 64, 0, st>>>(c, KT, total, units[0], units[1], units[2]);
-    else w4_stream_kernel<G, MT, R, NW, false, PAIR, EXPERTS><<<grid, NW * 64, 0, st>>>(c, KT, total, units[0], units[1], units[2]);
+    const unsigned grid = (unsigned)(w4_blocks(FORM, c, EXPERTS) * units);
+    if (zp)
+        w4_stream_kernel<G, MT, R, NW, D, true, PAIR, EXPERTS><<<grid, NW * 64, 0, st>>>(c, KT, (int)units, u[0], u[1], u[2]);
+    else
+        w4_stream_kernel<G, MT, R, NW, D, false, PAIR, EXPERTS><<<grid, NW * 64, 0, st>>>(c, KT, (int)units, u[0], u[1], u[2]);
     return hipGetLastError();
 }
 
 template <int G, bool PAIR, bool EXPERTS>
-hipError_t by_rows(const W4Call& c, hipStream_t st) {
-    constexpr int R = PAIR ? 2 : 1;
-    const int64_t m = EXPERTS ? c.block_rows : c.M;
-    if (m <= 16) return run<G, 1, R, 8, PAIR, EXPERTS>(c, st);
-    if (m <= 32) return run<G, 2, R, 8, PAIR, EXPERTS>(c, st);
-    return run<G, 4, 2, 4, PAIR, EXPERTS>(c, st);
+hipError_t by_form(int form, const W4Call& c, hipStream_t st) {
+    constexpr int D4 = G == 128 ? 2 : 1;   // two blocks of four row tiles: too many registers with more scales
+    if constexpr (!PAIR)
+        if (form == kW4Stream16x1) return run<G, kW4Stream16x1, 8, 2, PAIR, EXPERTS>(c, st);
+    if (form <= kW4Stream16x2) return run<G, kW4Stream16x2, 8, 2, PAIR, EXPERTS>(c, st);
+    if (form == kW4Stream16x4) return run<G, kW4Stream16x4, 8, 1, PAIR, EXPERTS>(c, st);
+    if (form == kW4Stream16x4W4) return run<G, kW4Stream16x4W4, 4, D4, PAIR, EXPERTS>(c, st);
+    return run<G, kW4Stream32x4, 8, 1, PAIR, EXPERTS>(c, st);
 }
 
 template <bool PAIR, bool EXPERTS>
-hipError_t by_group(const W4Call& c, hipStream_t st) {
-    if (c.group == 32) return by_rows<32, PAIR, EXPERTS>(c, st);
-    if (c.group == 64) return by_rows<64, PAIR, EXPERTS>(c, st);
-    return by_rows<128, PAIR, EXPERTS>(c, st);
+hipError_t by_group(int form, const W4Call& c, hipStream_t st) {
+    if (c.group == 32) return by_form<32, PAIR, EXPERTS>(form, c, st);
+    if (c.group == 64) return by_form<64, PAIR, EXPERTS>(form, c, st);
+    return by_form<128, PAIR, EXPERTS>(form, c, st);
 }
 
 // Row-major weights to the packed order: one thread per packed dword of
@@ -354,9 +370,9 @@ hipError_t launch_pack_w4(const uint8_t* q, const uint16_t* s, const uint8_t* z,
     return hipGetLastError();
 }
 
-hipError_t launch_w4_stream(const W4Call& c, bool pair, bool experts, hipStream_t st) {
-    if (pair) return experts ? by_group<true, true>(c, st) : by_group<true, false>(c, st);
-    return experts ? by_group<false, true>(c, st) : by_group<false, false>(c, st);
+hipError_t launch_w4_stream(int form, const W4Call& c, bool pair, bool experts, hipStream_t st) {
+    if (pair) return experts ? by_group<true, true>(form, c, st) : by_group<true, false>(form, c, st);
+    return experts ? by_group<false, true>(form, c, st) : by_group<false, false>(form, c, st);
 }
 
 hipError_t launch_experts_down_direct(const W4Call& c, const float* weights, int64_t T, int k, uint16_t* y,
