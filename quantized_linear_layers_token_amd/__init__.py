@@ -362,6 +362,9 @@ def qlin_linear_swiglu(scheme, x, gate, up, h, q_x=None, s_x=None, stream=None):
 # current, on `stream` or that device's current stream.
 # --------------------------------------------------------------------------
 
+import torch as _torch  # noqa: E402  (loaded with the library above)
+
+
 class W4Weight:
     """4-bit weights laid out for the library by qlin_pack_w4: one matrix
     [N, K], or `experts` of them.  Owns the packed tensors."""
@@ -374,39 +377,41 @@ class W4Weight:
         self._ref = ctypes.byref(self._struct)
 
 
-def _launch(name, device, stream, *args):
-    import torch
+# Handle of a device's current stream, without building a Stream object where torch offers that.
+_raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: _torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(fn, device, stream, *args):
     if device.type != "cuda":
         raise ValueError("the tensors must be device tensors")
     index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(index).cuda_stream
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    fn = getattr(_lib, name)
-    if index == torch.cuda.current_device():
+    if index == _torch.cuda.current_device():
         status = fn(*args, stream)
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(index):
             status = fn(*args, stream)
     if status != QLIN_OK:
-        raise QlinError(status, name)
+        raise QlinError(status, fn.__name__)
 
 
 def _w4_tensor(t, name, shape, size, device):
     """One tensor argument of the calls below: exactly this shape (None: any), contiguous, on the call's device."""
-    if not t.is_contiguous() or t.element_size() != size or (shape is not None and tuple(t.shape) != shape):
+    if t.element_size() != size or (shape is not None and t.shape != shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {size}-byte elements"
                          + (f" and shape {list(shape)}, not {list(t.shape)}" if shape is not None else ""))
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
 
 
-def qlin_pack_w4(q_w, s_w, z_w=None, stream=None):
+def qlin_pack_w4(q_w, s_w, z_w=None):
     """q_w uint8 [N, K/2] (input 2 i in the low half of byte i) or [E, N, K/2],
     s_w bf16 [.., N, K/group], z_w uint8 like s_w or None (8) -> W4Weight.
-    The packed weights are new tensors; the arguments need not be kept."""
-    import torch
+    The packed weights are new tensors, written on the current stream; the arguments need not be kept."""
     if q_w.dim() not in (2, 3) or s_w.dim() != q_w.dim():
         raise ValueError("q_w must be [N, K/2] or [E, N, K/2], s_w [N, K/group] or [E, N, K/group]")
     E, N, K = (q_w.shape[0] if q_w.dim() == 3 else 1), q_w.shape[-2], 2 * q_w.shape[-1]
@@ -422,35 +427,42 @@ def qlin_pack_w4(q_w, s_w, z_w=None, stream=None):
     if (N and not size) or E > MAX_EXPERTS:
         raise QlinError(QLIN_ERR_SHAPE, "qlin_pack_w4")
     count = E * _lib.qlin_w4_packed_scales(N, K, group)
-    packed = torch.empty((E * size,), dtype=torch.uint8, device=q_w.device)
-    scales = torch.empty((count,), dtype=s_w.dtype, device=q_w.device)
-    zeros = None if z_w is None else torch.empty((count,), dtype=z_w.dtype, device=q_w.device)
-    _launch("qlin_pack_w4", q_w.device, stream, q_w.data_ptr(), s_w.data_ptr(), _ptr(z_w), E, N, K, group, packed.data_ptr(),
+    packed = _torch.empty((E * size,), dtype=_torch.uint8, device=q_w.device)
+    scales = _torch.empty((count,), dtype=s_w.dtype, device=q_w.device)
+    zeros = None if z_w is None else _torch.empty((count,), dtype=z_w.dtype, device=q_w.device)
+    _launch(_lib.qlin_pack_w4, q_w.device, None, q_w.data_ptr(), s_w.data_ptr(), _ptr(z_w), E, N, K, group, packed.data_ptr(),
             scales.data_ptr(), _ptr(zeros))
     return W4Weight(packed, scales, zeros, E, N, K, group)
 
 
 def _w4_input(x, w, name):
-    if x.dim() != 2 or not x.is_contiguous() or x.element_size() != 2:
+    if x.dim() != 2 or x.element_size() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D tensor of 2-byte elements")
     if w.K != x.shape[1] or w.device != x.device:
         raise ValueError(f"{name} has {w.K} inputs on {w.device}, x {x.shape[1]} on {x.device}")
 
 
+_W4_ARRAYS = [(QlinW4Weight * n, _P * n) for n in range(MAX_SEGMENTS + 1)]
+
+
 def qlin_linear_w4(x, segments, out=OUT_BF16, stream=None):
     """x bf16 [M, K]; segments: list of (W4Weight [n, K], y [M, n]) sharing x, of one group size."""
-    M, K = x.shape
     nw = len(segments)
-    weights, ys = (QlinW4Weight * nw)(), (_P * nw)()
-    size = _out_bytes(out)
-    for i, (w, y) in enumerate(segments):
-        _w4_input(x, w, f"segment {i}")
-        if w.experts != 1 or w.group != segments[0][0].group:
+    if not 1 <= nw <= MAX_SEGMENTS:
+        raise ValueError(f"segments must hold one to {MAX_SEGMENTS} (weight, y) pairs")
+    device, (M, K), group, size = x.device, x.shape, segments[0][0].group, _out_bytes(out)
+    for w, y in segments:
+        _w4_input(x, w, "a segment")
+        if w.experts != 1 or w.group != group:
             raise ValueError("every segment must be one matrix, all of one group size")
-        _w4_tensor(y, f"segment {i} y", (M, w.N), size, x.device)
-        weights[i] = w._struct
-        ys[i] = y.data_ptr()
-    _launch("qlin_linear_w4", x.device, stream, x.data_ptr(), M, K, segments[0][0].group if nw else 128, weights, ys, nw, out)
+        _w4_tensor(y, "a segment's y", (M, w.N), size, device)
+    if nw == 1:
+        weights, ys = w._ref, ctypes.byref(_P(y.data_ptr()))
+    else:
+        weight_array, pointer_array = _W4_ARRAYS[nw]
+        weights = weight_array(*[w._struct for w, _ in segments])
+        ys = pointer_array(*[y.data_ptr() for _, y in segments])
+    _launch(_lib.qlin_linear_w4, device, stream, x.data_ptr(), M, K, group, weights, ys, nw, out)
 
 
 def qlin_linear_swiglu_w4(x, gate, up, h, stream=None):
@@ -461,26 +473,25 @@ def qlin_linear_swiglu_w4(x, gate, up, h, stream=None):
     if gate.experts != 1 or up.experts != 1 or gate.N != up.N or gate.group != up.group:
         raise ValueError("gate and up must be one matrix each, of one shape and group size")
     _w4_tensor(h, "h", (M, gate.N), 2, x.device)
-    _launch("qlin_linear_swiglu_w4", x.device, stream, x.data_ptr(), M, K, gate.group, gate._ref, up._ref, h.data_ptr())
+    _launch(_lib.qlin_linear_swiglu_w4, x.device, stream, x.data_ptr(), M, K, gate.group, gate._ref, up._ref, h.data_ptr())
 
 
 def qlin_route(logits, ids, weights, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, group_best=2,
                renormalize=True, scale=1.0, stream=None):
     """logits bf16 or f32 [T, E]; ids int32 [T, k] and weights f32 [T, k] receive the k experts of each token."""
-    import torch
-    if logits.dim() != 2 or not logits.is_contiguous() or logits.dtype not in (torch.bfloat16, torch.float32):
+    if logits.dim() != 2 or not logits.is_contiguous() or logits.dtype not in (_torch.bfloat16, _torch.float32):
         raise ValueError("logits must be a contiguous 2-D tensor of bfloat16 or float32")
     T, E = logits.shape
-    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or weights.dtype != torch.float32:
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != _torch.int32 or weights.dtype != _torch.float32:
         raise ValueError("ids must be int32 [T, k] and weights float32 [T, k]")
     k = ids.shape[1]
     _w4_tensor(ids, "ids", None, 4, logits.device)
     _w4_tensor(weights, "weights", (T, k), 4, logits.device)
     if bias is not None:
-        if bias.dtype != torch.float32:
+        if bias.dtype != _torch.float32:
             raise ValueError("bias must be float32 [E]")
         _w4_tensor(bias, "bias", (E,), 4, logits.device)
-    _launch("qlin_route", logits.device, stream, logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, T, E,
+    _launch(_lib.qlin_route, logits.device, stream, logits.data_ptr(), OUT_F32 if logits.dtype == _torch.float32 else OUT_BF16, T, E,
             k, score, _ptr(bias), groups, top_groups, group_best, 1 if renormalize else 0, scale, ids.data_ptr(),
             weights.data_ptr())
 
@@ -496,7 +507,6 @@ def qlin_experts_w4_workspace(T, k, gate, up, down):
 def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
     """x bf16 [T, H]; ids int32 [T, k] (outside 0..E-1: no expert), weights f32 [T, k]; gate, up: W4Weight of E
     matrices [I, H], down of E matrices [H, I]; y bf16 [T, H]; workspace uint8, qlin_experts_w4_workspace bytes."""
-    import torch
     _w4_input(x, gate, "gate")
     T, H = x.shape
     E, I, group = gate.experts, gate.N, gate.group
@@ -504,7 +514,7 @@ def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
         raise ValueError("up must have gate's shape, down be [E, H, I], all of one group size")
     if up.device != x.device or down.device != x.device:
         raise ValueError(f"every tensor must be on {x.device}")
-    if ids.dim() != 2 or ids.dtype != torch.int32 or weights.dtype != torch.float32:
+    if ids.dim() != 2 or ids.dtype != _torch.int32 or weights.dtype != _torch.float32:
         raise ValueError("ids must be int32 [T, k] and weights float32 [T, k]")
     k = ids.shape[1]
     device = x.device
@@ -515,5 +525,5 @@ def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
     need = _lib.qlin_experts_w4_workspace(T, k, E, H, I)
     if workspace.numel() < need:
         raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
-    _launch("qlin_experts_w4", device, stream, x.data_ptr(), T, H, I, E, k, group, ids.data_ptr(), weights.data_ptr(),
+    _launch(_lib.qlin_experts_w4, device, stream, x.data_ptr(), T, H, I, E, k, group, ids.data_ptr(), weights.data_ptr(),
             gate._ref, up._ref, down._ref, y.data_ptr(), workspace.data_ptr())
