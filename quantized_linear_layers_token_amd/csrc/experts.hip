@@ -8,11 +8,15 @@ namespace {
 
 // One workgroup counts the slots of each expert, places the experts one after
 // the other, and writes the slots in that order, those of one expert in the
-// order of their tokens: the same for every run, with no atomics.  Each
-// wavefront owns a contiguous share of the slots.  Lanes with equal experts
-// find each other by one ballot per bit of the expert.
-constexpr int kPlanWaves = 8;
-constexpr int kPlanBatch = 8;        // loads in flight per lane
+// order of their tokens: the same for every run.  Each wavefront owns a
+// contiguous share of the slots, kept in registers between the two passes
+// where 1024 per wavefront hold it (16384 slots: 28 us with half the
+// wavefronts and the ids read again, 8 loads in flight; bound by their
+// latency).  The counts are integer sums (LDS atomics: any order gives the
+// same); for the places, lanes with equal experts find each other by one
+// ballot per bit of the expert.
+constexpr int kPlanWaves = 16;
+constexpr int kPlanBatch = 16;       // loads in flight per lane
 template <int BITS>
 __global__ __launch_bounds__(kPlanWaves * 64) void experts_plan_kernel(const int32_t* __restrict__ ids, int64_t slots, int E,
                                                                       int block_rows, int* __restrict__ order,
@@ -23,39 +27,25 @@ __global__ __launch_bounds__(kPlanWaves * 64) void experts_plan_kernel(const int
     __shared__ int wsum[2][kPlanWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (int i = tid; i < kPlanWaves * EP; i += kPlanWaves * 64) (&count[0][0])[i] = 0;
-    __syncthreads();
-
     const int64_t chunks = (slots + 63) / 64, per = (chunks + kPlanWaves - 1) / kPlanWaves;
     const int64_t c0 = wave * per, c1 = c0 + per < chunks ? c0 + per : chunks;
-    auto pass = [&](auto use) {
-        for (int64_t c = c0; c < c1; c += kPlanBatch) {
-            int id[kPlanBatch];
+    int id[kPlanBatch];
+    auto load = [&](int64_t c) {
 #pragma unroll
-            for (int b = 0; b < kPlanBatch; ++b) {
-                const int64_t i = (c + b) * 64 + lane;
-                id[b] = c + b < c1 && i < slots ? ids[i] : -1;
-            }
-#pragma unroll
-            for (int b = 0; b < kPlanBatch; ++b) {
-                const bool live = (unsigned)id[b] < (unsigned)E;
-                uint64_t same = __ballot(live);
-                if (!same) continue;
-#pragma unroll
-                for (int bit = 0; bit < BITS; ++bit) {
-                    const bool on = (id[b] >> bit) & 1;
-                    const uint64_t v = __ballot(on);
-                    same &= on ? v : ~v;
-                }
-                if (live) use((c + b) * 64 + lane, id[b], same);
-                __builtin_amdgcn_wave_barrier();
-                __threadfence_block();
-            }
+        for (int b = 0; b < kPlanBatch; ++b) {
+            const int64_t i = (c + b) * 64 + lane;
+            id[b] = c + b < c1 && i < slots ? ids[i] : -1;
         }
     };
-    pass([&](int64_t, int e, uint64_t same) {
-        if (lane == __builtin_ctzll(same)) count[wave][e] += __popcll(same);
-    });
+    load(c0);
+    for (int i = tid; i < kPlanWaves * EP; i += kPlanWaves * 64) (&count[0][0])[i] = 0;
+    __syncthreads();
+    for (int64_t c = c0; c < c1; c += kPlanBatch) {
+        if (c > c0) load(c);
+#pragma unroll
+        for (int b = 0; b < kPlanBatch; ++b)
+            if ((unsigned)id[b] < (unsigned)E) atomicAdd(&count[wave][id[b]], 1);
+    }
     __syncthreads();
 
     // per expert: rows and items, then their sums over the experts before it
@@ -120,18 +110,37 @@ __global__ __launch_bounds__(kPlanWaves * 64) void experts_plan_kernel(const int
         items[3 * i + 2] = min(block_rows, first[e + 1] - begin);
     }
 
-    pass([&](int64_t i, int e, uint64_t same) {
-        const int place = first[e] + count[wave][e] + __popcll(same & ((uint64_t(1) << lane) - 1));
-        order[place] = (int)i;
-        // the count moves on after every lane of the group has read it
-        __builtin_amdgcn_wave_barrier();
-        if (lane == __builtin_ctzll(same)) count[wave][e] += __popcll(same);
-    });
+    for (int64_t c = c0; c < c1; c += kPlanBatch) {
+        if (per > kPlanBatch) load(c);
+#pragma unroll
+        for (int b = 0; b < kPlanBatch; ++b) {
+            const int e = id[b];
+            const bool live = (unsigned)e < (unsigned)E;
+            uint64_t same = __ballot(live);
+            if (!same) continue;
+#pragma unroll
+            for (int bit = 0; bit < BITS; ++bit) {
+                const bool on = (e >> bit) & 1;
+                const uint64_t v = __ballot(on);
+                same &= on ? v : ~v;
+            }
+            if (live) {
+                const int before = count[wave][e];
+                order[first[e] + before + __popcll(same & ((uint64_t(1) << lane) - 1))] = (int)((c + b) * 64 + lane);
+                // the count moves on after every lane of the group has read it
+                __builtin_amdgcn_wave_barrier();
+                if (lane == __builtin_ctzll(same)) count[wave][e] = before + __popcll(same);
+            }
+            __builtin_amdgcn_wave_barrier();
+            __threadfence_block();
+        }
+    }
 }
 
 // y[t] = sum_j weights[t, j] * rows[t * k + j]: four outputs per thread, the
 // slots in order.  Bound by reading the f32 rows (they stay f32: one rounding
-// of the sum instead of one per expert).
+// of the sum instead of one per expert).  Eight rows are read at once; those of
+// slots without an expert hold anything and are dropped after the read.
 __global__ __launch_bounds__(256) void experts_combine_kernel(const float* __restrict__ rows, const int32_t* __restrict__ ids,
                                                              const float* __restrict__ weights, int64_t T, int k, int E,
                                                              int64_t H, uint16_t* __restrict__ y) {
@@ -139,13 +148,22 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(const float* __res
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t t = i / quads, h = (i % quads) * 4;
         float v[4] = {};
-        for (int j = 0; j < k; ++j) {
-            const int64_t s = t * k + j;
-            if ((unsigned)ids[s] >= (unsigned)E) continue;
-            const float w = weights[s];
-            const v4f r = *reinterpret_cast<const v4f*>(rows + s * H + h);
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            v4f r[8];
+            float w[8];
+            bool live[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(w, r[c], v[c]);
+            for (int j = 0; j < 8; ++j) {
+                const int64_t s = t * k + min(j0 + j, k - 1);
+                r[j] = *reinterpret_cast<const v4f*>(rows + s * H + h);
+                w[j] = weights[s];
+                live[j] = j0 + j < k && (unsigned)ids[s] < (unsigned)E;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (live[j])
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(w[j], r[j][c], v[c]);
         }
         store4_f32(y, t * H + h, v, OUT_BF16);
     }

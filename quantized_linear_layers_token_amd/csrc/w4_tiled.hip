@@ -26,6 +26,8 @@ __device__ __forceinline__ uint32_t again(uint32_t v) {
 
 constexpr int kPanelGroup = 8;   // panels that take turns on the same rows of x (their weights stay in the XCD's L2)
 
+constexpr int kItemGroup = 4;    // items that take turns on the same panel
+
 template <int G, int RT, int KG, bool ZP, bool PAIR, bool EXPERTS>
 __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT, int panels, int panels0, int panels1, int panels2,
                                                           int row_blocks) {
@@ -42,19 +44,28 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
     const int lane = tid & 63;
     const int q = lane >> 4, col = lane & 15;
 
-    // Workgroup b runs on XCD b % 8: each XCD takes a contiguous part of the
-    // tiles, ordered so that kPanelGroup panels run over the same rows of x.
-    if constexpr (EXPERTS) row_blocks = *c.nitems;
-    const int ntiles = row_blocks * panels;
+    // Workgroup b runs on XCD b % 8.  Dense: each XCD takes a contiguous part of
+    // the tiles, ordered so that kPanelGroup panels run over the same rows of x.
+    // Experts: kItemGroup items in a row (most often one expert's) to an XCD, so
+    // that they read its weights there once, and the XCDs in turn, so that each
+    // has its share however many items there are.
     const int b = blockIdx.x;
-    if (b >= ntiles) return;
-    const int per = ntiles >> 3, extra = ntiles & 7, xcd = b & 7;
-    const int t = xcd * per + min(xcd, extra) + (b >> 3);
-    const int band = t / (kPanelGroup * row_blocks);
-    const int width = min(kPanelGroup, panels - band * kPanelGroup);
-    const int in_band = t - band * kPanelGroup * row_blocks;
-    const int block = __builtin_amdgcn_readfirstlane(in_band / width);
-    int panel = __builtin_amdgcn_readfirstlane(band * kPanelGroup + in_band % width), seg = 0;
+    int panel, block, seg = 0;
+    if constexpr (EXPERTS) {
+        const int at = b >> 3, group = at / (kItemGroup * panels), in_group = at - group * (kItemGroup * panels);
+        panel = __builtin_amdgcn_readfirstlane(in_group / kItemGroup);
+        block = __builtin_amdgcn_readfirstlane((group * 8 + (b & 7)) * kItemGroup + in_group % kItemGroup);
+        if (block >= *c.nitems) return;
+    } else {
+        const int ntiles = row_blocks * panels;
+        const int per = ntiles >> 3, extra = ntiles & 7, xcd = b & 7;
+        const int t = xcd * per + min(xcd, extra) + (b >> 3);
+        const int band = t / (kPanelGroup * row_blocks);
+        const int width = min(kPanelGroup, panels - band * kPanelGroup);
+        const int in_band = t - band * kPanelGroup * row_blocks;
+        block = __builtin_amdgcn_readfirstlane(in_band / width);
+        panel = __builtin_amdgcn_readfirstlane(band * kPanelGroup + in_band % width);
+    }
     if constexpr (!PAIR && !EXPERTS) {
         if (panel >= panels0) { panel -= panels0; seg = 1; }
         if (seg == 1 && panel >= panels1) { panel -= panels1; seg = 2; }
@@ -295,7 +306,8 @@ hipError_t run(const W4Call& c, hipStream_t st) {
         p[i] = (int)((w4_row_tiles(c.n[i]) + PT - 1) / PT);
         zp |= c.z[i] != nullptr;
     }
-    const unsigned grid = (unsigned)((int64_t)blocks * panels);
+    constexpr int64_t round = 8 * kItemGroup;
+    const unsigned grid = (unsigned)((EXPERTS ? (blocks + round - 1) / round * round : (int64_t)blocks) * panels);
     if (zp) w4_tiled_kernel<G, RT, KG, true, PAIR, EXPERTS><<<grid, 256 * KG, 0, st>>>(c, KT, panels, p[0], p[1], p[2], blocks);
     else w4_tiled_kernel<G, RT, KG, false, PAIR, EXPERTS><<<grid, 256 * KG, 0, st>>>(c, KT, panels, p[0], p[1], p[2], blocks);
     return hipGetLastError();
