@@ -127,12 +127,14 @@ int64_t qlin_experts_w4_workspace(int64_t T, int32_t k, int64_t E, int64_t H, in
 
 /* The gated MLP of the chosen experts, summed with the router's weights:
  *   y[t] = bf16( sum_j weights[t, j] * W_down[e] h_j ),  e = ids[t, j],
- *   h_j = bf16( silu(W_gate[e] x_t) * (W_up[e] x_t) )
+ *   h_j = silu(W_gate[e] x_t) * (W_up[e] x_t)
  * over the slots j whose ids[t, j] is in [0, E); any other id (e.g. -1 for
  * tokens that pad a batch, or experts that live elsewhere) adds nothing, and a
  * token without experts gets zeros.  An expert may be chosen twice.  h is the
- * only value rounded on the way (it is a matrix-core operand); the sums,
- * including the one over the experts, are f32 in the order of j.
+ * only value rounded on the way (it is a matrix-core operand): to bf16 where
+ * many rows share an expert's weights and the matrix cores bound the call, to
+ * two bf16 parts (16 bits) where they do not.  The sums, including the one over
+ * the experts, are f32 in the order of j.
  *   x bf16 [T, H]; ids [T, k], weights f32 [T, k] (qlin_route writes both);
  *   gate, up: E matrices [I, H]; down: E matrices [H, I]; one group size for
  *   all three (H and I multiples of it); y bf16 [T, H].

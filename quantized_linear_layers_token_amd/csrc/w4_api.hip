@@ -257,7 +257,7 @@ Workspace layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     w.items = w.order + (direct ? 0 : pad(4 * slots));
     w.nitems = w.items + (direct ? 0 : pad(12 * max_items(slots, E, 16)));
     w.h = w.nitems + (direct ? 0 : 256);
-    w.rows = w.h + pad(2 * slots * I);
+    w.rows = w.h + pad(4 * slots * I);   // two bf16 parts
     w.bytes = w.rows + (direct ? 0 : pad(4 * slots * H));
     return w;
 }

@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t w4_zeros(__amdgpu_buffer_rsrc_t d, int lane_
     else return __builtin_amdgcn_raw_buffer_load_b32(d, lane_at, block_at, 0);
 }
 
-// silu(g) * u of the f32 sums, rounded once.
-__device__ __forceinline__ uint16_t swiglu_f32(float g, float u) { return f32_to_bf16(g / (1.0f + __expf(-g)) * u); }
+// silu(g) * u of the f32 sums.
+__device__ __forceinline__ float swiglu_f32(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
 }  // namespace qlin

@@ -57,7 +57,10 @@ constexpr int kW4FormRows[kW4Forms] = {16, 16, 16, 16, 32, 64, 64};
 constexpr int kW4FormTiles[kW4Forms] = {1, 2, 4, 4, 4, 8, 16};
 constexpr int kW4FormThreads[kW4Forms] = {512, 512, 512, 256, 512, 512, 256};
 
-// y (or, with pair, h = silu(x w[0]^T) * (x w[1]^T)) in the given form.
+// y (or, with pair, h = silu(x w[0]^T) * (x w[1]^T)) in the given form.  Between
+// the two products of the experts, the streaming forms write and read h as two
+// bf16 parts, [rows][2][n]: h rounded to bf16, and what that left (16 bits of
+// h; the matrix cores have the time).  The tiled forms keep the first alone.
 hipError_t launch_w4_stream(int form, const W4Call& c, bool pair, bool experts, hipStream_t st);
 hipError_t launch_w4_tiled(int form, const W4Call& c, bool pair, bool experts, hipStream_t st);
 

@@ -27,6 +27,7 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
     constexpr int SL = G / 32;                    // 32-input slices of a group
     constexpr int T = MT * 16;
     constexpr int RM = PAIR ? R / 2 : R;          // row tiles of each matrix
+    constexpr int P = EXPERTS && !PAIR ? 2 : 1;   // bf16 parts of an input (the experts' h comes in two)
     __shared__ __attribute__((aligned(16))) float red[NW * R * T * 16];
 
     const int tid = threadIdx.x;
@@ -73,7 +74,7 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int64_t r = row_of(min(mt * 16 + col, rows - 1));
-        xp[mt] = (Global<uint16_t>)c.x + (EXPERTS ? r / c.xdiv : r) * K + q * 8;
+        xp[mt] = (Global<uint16_t>)c.x + (PAIR && EXPERTS ? r / c.xdiv : r) * (P * K) + q * 8;
     }
 
     // this wavefront's share of the inputs: n blocks from k0.  Descriptors that
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
     v4f tot[R][MT] = {};
 
     v4u w[D][R];
-    v8bf a[D][MT][4];
+    v8bf a[D][MT][P][4];
     W4Scales<SUB> s[D][R];
     uint32_t z[D][R];
     auto load = [&](int d, int i) {
@@ -112,7 +113,9 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) a[d][mt][j] = *(Global<v8bf>)(xp[mt] + 32 * min(4 * (k0 + i) + j, last));
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int p = 0; p < P; ++p) a[d][mt][p][j] = *(Global<v8bf>)(xp[mt] + p * K + 32 * min(4 * (k0 + i) + j, last));
     };
     auto multiply = [&](int d) {
 #pragma unroll
@@ -121,7 +124,9 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int j = 0; j < SL; ++j) c0[mt] = mfma_bf16(a[d][mt][g * SL + j], ones, c0[mt]);
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int j = 0; j < SL; ++j) c0[mt] = mfma_bf16(a[d][mt][p][g * SL + j], ones, c0[mt]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 v4f acc[MT];
@@ -138,7 +143,9 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
                 for (int j = 0; j < SL; ++j) {
                     const v8bf b = w4_codes(w[d][r][g * SL + j]);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_bf16(a[d][mt][g * SL + j], b, acc[mt]);
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) acc[mt] = mfma_bf16(a[d][mt][p][g * SL + j], b, acc[mt]);
                 }
                 const float sf = s[d][r].at(g);
 #pragma unroll
@@ -191,9 +198,14 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
         const int nn = tile0 * 16 + n;
         if (nn >= N) continue;
         const int at = t * 16 + (n & 15);
-        const int64_t o = row_of(t) * N + nn;
-        if constexpr (PAIR) static_cast<uint16_t*>(c.y[0])[o] = swiglu_f32(sum(r, at), sum(r + RM, at));
-        else store_f32(EXPERTS ? c.y[0] : pick_ptr(c.y, seg), o, sum(r, at), c.mode);
+        const int64_t o = row_of(t) * (PAIR && EXPERTS ? 2 * (int64_t)N : (int64_t)N) + nn;
+        if constexpr (PAIR) {
+            const float h = swiglu_f32(sum(r, at), sum(r + RM, at));
+            uint16_t* y = static_cast<uint16_t*>(c.y[0]);
+            const uint16_t hi = f32_to_bf16(h);
+            y[o] = hi;
+            if constexpr (EXPERTS) y[o + N] = f32_to_bf16(h - bf16_lo(hi));
+        } else store_f32(EXPERTS ? c.y[0] : pick_ptr(c.y, seg), o, sum(r, at), c.mode);
     }
 }
 
@@ -201,7 +213,9 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
 //   y[t, n] = sum_j weights[t, j] * sum_k h[t * k + j, k] * w[ids[t, j]][n, k].
 // A workgroup takes one token and 16 output rows; its wavefronts share out the
 // (slot, 128-input block) pairs, so that a single token still keeps every load
-// of its 16 rows in flight, and no row of a slot passes through memory.
+// of its 16 rows in flight, and no row of a slot passes through memory.  The
+// operand's 16 rows are the two parts of h in turn: the sums of rows 0 and 1
+// are those of one part each.
 template <int G, int NW, bool ZP>
 __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int KT, int units, const float* __restrict__ weights,
                                                                  int k, uint16_t* __restrict__ y) {
@@ -239,7 +253,7 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
             const int64_t ee = live[u] ? e : 0;    // a slot without an expert reads expert 0 and is dropped
             w[u] = __builtin_nontemporal_load(
                 reinterpret_cast<const v4u*>(c.w[0] + ((ee * units + tile) * KT + kb[u]) * kW4Block + lane * 16));
-            const uint16_t* xr = c.x + (t * k + j) * (int64_t)K + q * 8;
+            const uint16_t* xr = c.x + ((t * k + j) * 2 + (col & 1)) * (int64_t)K + q * 8;
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[u][i] = *reinterpret_cast<const v8bf*>(xr + 32 * min(4 * kb[u] + i, slices - 1));
             const int64_t sat = (((ee * units + tile) * KT + kb[u]) * 16 + col) * SUB;
@@ -259,8 +273,7 @@ __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int K
                 if constexpr (ZP) acc *= (float)((z[u] >> (8 * g)) & 255u);
 #pragma unroll
                 for (int j = 0; j < SL; ++j) acc = mfma_bf16(a[u][g * SL + j], w4_codes(w[u][g * SL + j]), acc);
-
-                part = __builtin_fmaf(s[u].at(g), acc[0], part);   // every row of the operand is the token
+                part = __builtin_fmaf(s[u].at(g), acc[0] + acc[1], part);
             }
             tot = __builtin_fmaf(wu[u], part, tot);
         }

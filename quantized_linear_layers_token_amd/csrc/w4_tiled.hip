@@ -288,7 +288,8 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
     };
     if constexpr (PAIR)
         store([&](int64_t at, int r, int mt, int i) {
-            ((__attribute__((address_space(1))) uint16_t*)y)[at] = swiglu_f32(tot[r][mt][i], tot[r + RM][mt][i]);
+            ((__attribute__((address_space(1))) uint16_t*)y)[at] =
+                f32_to_bf16(swiglu_f32(tot[r][mt][i], tot[r + RM][mt][i]));
         });
     else if (c.mode == OUT_F32)
         store([&](int64_t at, int r, int mt, int i) { ((__attribute__((address_space(1))) float*)y)[at] = tot[r][mt][i]; });

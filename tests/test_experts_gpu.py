@@ -196,3 +196,14 @@ def test_a_layer_of_them_together_eager_and_replayed(T):
         torch.cuda.synchronize()
         for o, e in zip(outs, eager):
             assert np.array_equal(host(o), e)
+
+
+@pytest.mark.parametrize("T,E,k,H,I,group,zeros", [(1, 16, 4, 256, 512, 128, False), (4, 6, 3, 128, 160, 32, True),
+                                                   (30, 24, 4, 256, 320, 64, True), (90, 12, 2, 128, 256, 128, False)])
+def test_few_rows_keep_16_bits_of_h(T, E, k, H, I, group, zeros):
+    """Where the weights are streamed (few rows of each expert), h goes on as a bf16 value and the bf16 rounding of
+    what that left: an error of at most 2^-8 * 2^-8 of h."""
+    xb, ids, wt, ws = make(10, T, E, k, H, I, group, zeros)
+    y = run(xb, ids, wt, ws)
+    ref, bound = R.experts(R.bf16_values(xb), ids, wt, *ws, group, h_half=2.0 ** -16)
+    assert (np.abs(y - ref) <= bound + R.BF16_HALF * (np.abs(ref) + bound)).all()
