@@ -9,10 +9,13 @@
 // Two scores that differ in the last bit of f32 decide which expert runs, so
 // everything that a choice depends on is f64 (full rate on this chip); where
 // the choice is the order of the logits themselves (no bias, and no group sums
-// of more than one) they are compared as they are.  Lane l holds the
-// experts l, l + 64, ...: the largest choice is a wavefront maximum, its first
-// holder a ballot per 64 experts.  Bound by the k rounds of that (some 30
-// instructions each) from a few hundred tokens on, below by the launch.
+// of more than one) they are compared as they are.  Lane l holds the experts
+// l, l + 64, ....  A round of the selection takes the wavefront maximum of
+// 32-bit keys (the choices rounded to f32, or the logits, as integers in their
+// order) and a ballot of its holders; only where several experts share the key
+// are their f64 choices compared.  Bound by vector instructions from some
+// thousand tokens on, below by the launch: 4096 tokens, 256 experts, sigmoid
+// and bias, the best 4 of 8 groups, 8 of 256.
 #include <cfloat>
 
 #include "qlin_device.h"
@@ -67,26 +70,38 @@ __device__ __forceinline__ double wave_sum(double v) {
     return (lane_d(v, 0) + lane_d(v, 16)) + (lane_d(v, 32) + lane_d(v, 48));
 }
 
-// The choices in their order, as numbers of type Key.  Below every choice of
-// an expert that takes part: kMasked (an expert that is masked out comes after
-// every other expert of the groups that stay), and below that kGone (experts of
-// dropped groups, and those taken already).
-template <class Key> struct Order;
-template <> struct Order<double> {           // scores and biases: no NaN, no infinity
-    static constexpr double kGone = -INFINITY, kMasked = -DBL_MAX;
-    static __device__ __forceinline__ double of(double v) { return v >= -DBL_MAX ? fmin(v, DBL_MAX) : -DBL_MAX; }
-};
-template <> struct Order<int> {              // logits: the bits of a float, in the order of its values
-    static constexpr int kGone = INT32_MIN, kMasked = INT32_MIN + 1;
-    static __device__ __forceinline__ int of(float v) {
-        const int b = __float_as_int(v + 0.0f);   // -0 equals 0
-        return b ^ ((b >> 31) & 0x7FFFFFFF);
-    }
-};
+// Keys: the bits of a float as an integer in the order of its values.  Below
+// that of every expert that takes part: kMasked (an expert that is masked out
+// comes after every other expert of the groups that stay), and below that kGone
+// (experts of dropped groups, and those taken already).
+constexpr int kGone = INT32_MIN, kMasked = INT32_MIN + 1;
+__device__ __forceinline__ int key_of(float v) {
+    const int b = __float_as_int(v + 0.0f);   // -0 equals 0
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+// A choice without NaN and infinities.
+__device__ __forceinline__ double finite(double v) { return v >= -DBL_MAX ? fmin(v, DBL_MAX) : -DBL_MAX; }
 
-// V: experts per lane.  Key: the type of the choice (double: from the scores,
-// int: the logits).
-template <int V, class Key, class Logit>
+// 1 / (1 + e^-l); 0 below l = -708, where e^-l nears the end of f64.
+__device__ __forceinline__ double sigmoid(float l) {
+    const double d = 1.0 + exp(-(double)fmaxf(l, -708.0f));
+    double r = __builtin_amdgcn_rcp(d);       // two Newton steps: within a unit or two of the last place
+    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+    return l < -708.0f ? 0.0 : r;
+}
+
+// The two largest of two lanes' two largest.
+template <int CTRL>
+__device__ __forceinline__ void merge_dpp(double& a, double& b) {
+    const double oa = dpp_d<CTRL>(a), ob = dpp_d<CTRL>(b);
+    b = fmax(fmin(a, oa), fmax(b, ob));
+    a = fmax(a, oa);
+}
+
+// V: experts per lane.  SCORES: the choices are f64 values from the scores
+// (else the logits).
+template <int V, bool SCORES, class Logit>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
     const Logit* __restrict__ logits, int64_t T, int E, int k, int score, const float* __restrict__ bias, int groups,
     int top_groups, int group_best, bool renorm, float scale, int32_t* __restrict__ ids, float* __restrict__ weights) {
@@ -115,38 +130,43 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
 #pragma unroll
         for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
         m = wave_max(m);
+        if (m == -INFINITY) m = 0.0f;    // every expert masked out: scores of zero
         double z = 0.0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            p[j] = l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)m);
+            p[j] = exp((double)l[j] - (double)m);
             z += p[j];
         }
         total = wave_sum(z);
-        if (total == 0.0) total = 1.0;   // every expert masked out
+        if (total == 0.0) total = 1.0;
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) p[j] = l[j] == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-(double)l[j]));
+        for (int j = 0; j < V; ++j) p[j] = sigmoid(l[j]);
     }
 
-    Key c[V];
+    int key[V];
+    double c[SCORES ? V : 1];
+    const double inv = 1.0 / total;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int e = j * 64 + lane;
-        if constexpr (sizeof(Key) == 8) {
-            double v = score == 0 ? p[j] / total : p[j];
+        if constexpr (SCORES) {
+            double v = p[j] * inv;
             if (bias && e < E) v += (double)bias[e];
-            c[j] = Order<Key>::of(v);
+            c[j] = l[j] == -INFINITY ? -DBL_MAX : finite(v);
+            // f32 rounding keeps the order; past its range every choice shares the last key
+            key[j] = key_of((float)fmax(fmin(c[j], (double)FLT_MAX), -(double)FLT_MAX));
         } else {
-            c[j] = Order<Key>::of(l[j]);
+            key[j] = key_of(l[j]);
         }
-        if (l[j] == -INFINITY) c[j] = Order<Key>::kMasked;
-        if (e >= E) c[j] = Order<Key>::kGone;
+        if (l[j] == -INFINITY) key[j] = kMasked;
+        if (e >= E) key[j] = kGone;
     }
 
     if (groups > 1) {
         const int size = E / groups;
 #pragma unroll
-        for (int j = 0; j < V; ++j) mine[j * 64 + lane] = sizeof(Key) == 8 ? (double)c[j] : l[j] == -INFINITY ? -DBL_MAX : (double)l[j];
+        for (int j = 0; j < V; ++j) mine[j * 64 + lane] = SCORES ? c[SCORES ? j : 0] : l[j] == -INFINITY ? -DBL_MAX : (double)l[j];
         __builtin_amdgcn_wave_barrier();
         __threadfence_block();
         // P lanes per group walk its experts and keep the two best
@@ -160,12 +180,16 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
                 b = fmax(b, fmin(a, v));
                 a = fmax(a, v);
             }
-        for (int d = 1; d < P; d <<= 1) {
+        if (P > 1) merge_dpp<0xB1>(a, b);
+        if (P > 2) merge_dpp<0x4E>(a, b);
+        if (P > 4) merge_dpp<0x141>(a, b);
+        if (P > 8) merge_dpp<0x140>(a, b);
+        for (int d = 16; d < P; d <<= 1) {
             const double oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
             b = fmax(fmin(a, oa), fmax(b, ob));
             a = fmax(a, oa);
         }
-        double worth = group_best == 2 && size > 1 ? Order<double>::of(a + b) : a;
+        double worth = group_best == 2 && size > 1 ? finite(a + b) : a;
         // a group stays if fewer than top_groups groups come before it
         int before = 0;
         for (int o = 0; o < groups; ++o) {
@@ -178,7 +202,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
         for (int j = 0; j < V; ++j) {
             const int e = j * 64 + lane;
             const int of = (int)(((uint64_t)e * magic) >> 21);
-            if (e < E && !((kept >> (of * P)) & 1)) c[j] = Order<Key>::kGone;
+            if (e < E && !((kept >> (of * P)) & 1)) key[j] = kGone;
         }
         __threadfence_block();
     }
@@ -187,19 +211,34 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
 
     int chosen = 0;   // lane r: the token's choice r
     for (int r = 0; r < k; ++r) {
-        Key m = c[0];
+        int m = key[0];
 #pragma unroll
-        for (int j = 1; j < V; ++j) m = m > c[j] ? m : c[j];
+        for (int j = 1; j < V; ++j) m = max(m, key[j]);
         m = wave_max(m);
-        int at = -1;
+        uint64_t held[V];
+        int holders = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t b = __ballot(c[j] == m);
-            if (at < 0 && b) at = j * 64 + __builtin_ctzll(b);
+            held[j] = __ballot(key[j] == m);
+            holders += __popcll(held[j]);
         }
+        if constexpr (SCORES) {
+            if (holders > 1 && m > kMasked) {   // (masked experts are equal)
+                double best = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < V; ++j) best = fmax(best, key[j] == m ? c[j] : -INFINITY);
+                best = wave_max(best);
+#pragma unroll
+                for (int j = 0; j < V; ++j) held[j] = __ballot(key[j] == m && c[j] == best);
+            }
+        }
+        int at = -1;   // the first holder
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j)
+            if (held[j]) at = j * 64 + __builtin_ctzll(held[j]);
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (j * 64 + lane == at) c[j] = Order<Key>::kGone;
+            if (j * 64 + lane == at) key[j] = kGone;
         if (lane == r) chosen = at;
     }
     __builtin_amdgcn_wave_barrier();
@@ -209,7 +248,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
         const double s = wave_sum(w);
         w = s > 0.0 ? w / s : 0.0;
     } else if (score == 0) {
-        w /= total;
+        w *= inv;
     }
     if (lane < k) {
         ids[t * k + lane] = chosen;
@@ -217,27 +256,27 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
     }
 }
 
-template <int V, class Key>
+template <int V, bool SCORES>
 hipError_t run(const void* logits, bool f32, int64_t T, int E, int k, int score, const float* bias, int groups,
                int top_groups, int group_best, bool renorm, float scale, int32_t* ids, float* weights, hipStream_t st) {
     const unsigned grid = (unsigned)((T + kRouteWaves - 1) / kRouteWaves);
     if (f32)
-        route_kernel<V, Key, float><<<grid, kRouteWaves * 64, 0, st>>>(static_cast<const float*>(logits), T, E, k, score, bias,
+        route_kernel<V, SCORES, float><<<grid, kRouteWaves * 64, 0, st>>>(static_cast<const float*>(logits), T, E, k, score, bias,
                                                                        groups, top_groups, group_best, renorm, scale, ids, weights);
     else
-        route_kernel<V, Key, uint16_t><<<grid, kRouteWaves * 64, 0, st>>>(static_cast<const uint16_t*>(logits), T, E, k, score,
+        route_kernel<V, SCORES, uint16_t><<<grid, kRouteWaves * 64, 0, st>>>(static_cast<const uint16_t*>(logits), T, E, k, score,
                                                                           bias, groups, top_groups, group_best, renorm, scale, ids,
                                                                           weights);
     return hipGetLastError();
 }
 
-template <class Key, class... A>
+template <bool SCORES, class... A>
 hipError_t by_experts(int E, A... a) {
-    if (E <= 64) return run<1, Key>(a...);
-    if (E <= 128) return run<2, Key>(a...);
-    if (E <= 256) return run<4, Key>(a...);
-    if (E <= 512) return run<8, Key>(a...);
-    return run<16, Key>(a...);
+    if (E <= 64) return run<1, SCORES>(a...);
+    if (E <= 128) return run<2, SCORES>(a...);
+    if (E <= 256) return run<4, SCORES>(a...);
+    if (E <= 512) return run<8, SCORES>(a...);
+    return run<16, SCORES>(a...);
 }
 
 }  // namespace
@@ -247,9 +286,9 @@ hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int k, i
                         hipStream_t st) {
     const bool by_score = bias != nullptr || (groups > 1 && group_best > 1);
     if (by_score)
-        return by_experts<double>(E, logits, f32, T, E, k, score, bias, groups, top_groups, group_best, renorm, scale, ids,
+        return by_experts<true>(E, logits, f32, T, E, k, score, bias, groups, top_groups, group_best, renorm, scale, ids,
                                   weights, st);
-    return by_experts<int>(E, logits, f32, T, E, k, score, bias, groups, top_groups, group_best, renorm, scale, ids, weights,
+    return by_experts<false>(E, logits, f32, T, E, k, score, bias, groups, top_groups, group_best, renorm, scale, ids, weights,
                              st);
 }
 

@@ -94,6 +94,8 @@ def test_biases_that_are_not_finite():
     bias[[1, 2, 3, 30]] = [np.inf, -np.inf, np.nan, np.inf]
     check(l, 5, score=1, bias=bias)
     check(l, 40 // 2, score=0, bias=bias, groups=2, top_groups=2)
+    l[:, [3, 7, 8]] = -np.inf              # masked experts come after one with the smallest bias
+    check(l, 32, score=1, bias=np.where(np.arange(40) > 20, -np.inf, bias).astype(np.float32)[:40], groups=1)
 
 
 def test_neighbouring_scores_are_told_apart():

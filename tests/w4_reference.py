@@ -101,7 +101,7 @@ def route(logits, k, score, bias, groups, top_groups, group_best, renorm, scale)
                 s = np.where(out, 0.0, 1 / (1 + np.exp(-l)))
             by_logit = bias is None and (groups == 1 or group_best == 1)
             c = l.copy() if by_logit else s + (0 if bias is None else bias.astype(np.float64))
-        c = np.where(out | np.isnan(c), -big, np.clip(c, -big, big))
+        c = np.where(out, -np.inf, np.where(np.isnan(c), -big, np.clip(c, -big, big)))   # masked: after every other
         size = E // groups
         worth = []
         for g in range(groups):
