@@ -18,6 +18,9 @@
  *    qlin_linear_weight_only): products of inputs and codes are exact, sums are
  *    f32 per group, scaled in f32 and added in f32.
  *  - Results do not depend on what else runs: the same call gives the same bits.
+ *  - A row of x with an infinity or NaN, or with values past 2^112 in magnitude
+ *    (whose sums leave f32), gives values that are not finite, or unspecified, in
+ *    its own rows of the result and nowhere else.
  */
 #ifndef QLIN_W4_H_
 #define QLIN_W4_H_
@@ -116,8 +119,8 @@ typedef enum qlin_score {
  * experts are all masked out gets weights 0.
  * 1 <= k <= min(QLIN_MAX_CHOICES, top_groups * E / groups), E <= QLIN_MAX_EXPERTS,
  * groups <= QLIN_MAX_GROUPS a divisor of E, 1 <= top_groups <= groups
- * (QLIN_ERR_SHAPE).  logits 16-byte aligned (any rows), ids and weights
- * 4-byte aligned.  T == 0 is a no-op. */
+ * (QLIN_ERR_SHAPE).  logits aligned to their type, ids and weights to 4 bytes.
+ * T == 0 is a no-op. */
 qlin_status qlin_route(const void* logits, qlin_out logits_type, int64_t T, int64_t E, int32_t k, qlin_score score,
                        const float* bias, int32_t groups, int32_t top_groups, int32_t group_best, int32_t renormalize,
                        float scale, int32_t* ids, float* weights, hipStream_t stream);

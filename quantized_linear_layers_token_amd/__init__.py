@@ -404,6 +404,8 @@ def _w4_tensor(t, name, shape, size, device):
     if t.element_size() != size or (shape is not None and t.shape != shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {size}-byte elements"
                          + (f" and shape {list(shape)}, not {list(t.shape)}" if shape is not None else ""))
+    if t.dtype is _torch.float16:
+        raise ValueError(f"{name} must be bfloat16 (or its bit patterns), not float16")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
 
@@ -436,8 +438,8 @@ def qlin_pack_w4(q_w, s_w, z_w=None):
 
 
 def _w4_input(x, w, name):
-    if x.dim() != 2 or x.element_size() != 2 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous 2-D tensor of 2-byte elements")
+    if x.dim() != 2 or x.element_size() != 2 or not x.is_contiguous() or x.dtype is _torch.float16:
+        raise ValueError("x must be a contiguous 2-D tensor of bfloat16 (or its bit patterns)")
     if w.K != x.shape[1] or w.device != x.device:
         raise ValueError(f"{name} has {w.K} inputs on {w.device}, x {x.shape[1]} on {x.device}")
 

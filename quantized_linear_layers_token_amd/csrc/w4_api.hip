@@ -54,14 +54,15 @@ constexpr int64_t kMaxElements = int64_t(1) << 40;
 // without zero points, group 32 with them; 64 lies between).  The streaming
 // forms' workgroups share a CU (a second one costs half of the first at
 // least); the tiled forms run one (64 x 8) or two (64 x 16) at a time.
-// Examples of both sides, us: 4096 x 4096, 64 rows: 19.6, 12.5, 9.7, 9.7, 13.4,
-// 29.1, 47.3 in the order of the forms, 16 x 4 chosen; 512 rows: 125, 72, 48,
-// 46, 40, 31.6, 47.6, 64 x 8 chosen; 2048 rows: 489, 268, 179, 181, 145, 117,
-// 73.6, 64 x 16 chosen.
+// Examples of both sides, us at 4096 x 4096 in the order of the forms: 64 rows
+// 19.6, 12.5, 9.74, 9.69, 13.4, 29.1, 47.3 (16 x 4 with four wavefronts chosen);
+// 512 rows 125, 72, 48, 46, 40, 31.6, 47.6 (64 x 8 chosen); 2048 rows 489, 268,
+// 179, 181, 145, 117, 73.6 (64 x 16 chosen).  Over 130 shapes off these the
+// choice was 5 % slower than the best form, in the geometric mean.
 struct FormCost {
     double first, more;
 };
-constexpr FormCost kCost128[qlin::kW4Forms] = {{4.0, 3.8}, {4.5, 4.5}, {6.0, 5.8}, {6.5, 5.6}, {10.2, 10.2}, {27, 29}, {44, 68}};
+constexpr FormCost kCost128[qlin::kW4Forms] = {{4.0, 3.8}, {4.5, 4.5}, {6.0, 5.8}, {5.9, 5.6}, {10.2, 10.2}, {27, 29}, {44, 68}};
 constexpr FormCost kCost32[qlin::kW4Forms] = {{5.0, 4.6}, {6.5, 6.6}, {8.0, 8.5}, {11, 7.7}, {12.5, 13}, {46, 37}, {95, 128}};
 
 double form_cost(int form, const qlin::W4Call& c, bool pair, int64_t blocks) {
@@ -227,7 +228,7 @@ qlin_status qlin_route(const void* logits, qlin_out logits_type, int64_t T, int6
     if (k < 1 || k > QLIN_MAX_CHOICES || k > top_groups * (E / groups)) return QLIN_ERR_SHAPE;
     if (T == 0) return QLIN_OK;
     if (!logits || !ids || !weights) return QLIN_ERR_NULL;
-    if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return QLIN_ERR_ALIGN;
+    if (!aligned(logits, logits_type == QLIN_OUT_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return QLIN_ERR_ALIGN;
     const Range rl = rng(logits, T * E * (logits_type == QLIN_OUT_F32 ? 4 : 2)), rb = rng(bias, bias ? 4 * E : 0);
     const Range ri = rng(ids, 4 * T * k), rw = rng(weights, 4 * T * k);
     if (overlap(ri, rl) || overlap(rw, rl) || overlap(ri, rb) || overlap(rw, rb) || overlap(ri, rw)) return QLIN_ERR_ALIAS;
