@@ -87,6 +87,13 @@ __device__ __forceinline__ uint32_t w4_zeros(__amdgpu_buffer_rsrc_t d, int lane_
     else return __builtin_amdgcn_raw_buffer_load_b32(d, lane_at, block_at, 0);
 }
 
+// The same value, unpacked anew at every use: held unpacked for the whole
+// block, the scales and zero points would take the registers of the sums.
+__device__ __forceinline__ uint32_t again(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // silu(g) * u of the f32 sums.
 __device__ __forceinline__ float swiglu_f32(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 

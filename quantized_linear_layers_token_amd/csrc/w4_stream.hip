@@ -22,7 +22,7 @@ constexpr int kAux = 2;   // buffer-load cache policy: streaming
 
 // D: blocks of 128 inputs whose loads are in flight per wavefront.
 template <int G, int MT, int R, int NW, int D, bool ZP, bool PAIR, bool EXPERTS>
-__global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, int units, int units0, int units1, int units2) {
+__global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT, int units, int units0, int units1, int units2) {
     constexpr int SUB = kW4K / G;                 // groups in a 128-input block
     constexpr int SL = G / 32;                    // 32-input slices of a group
     constexpr int T = MT * 16;
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
     const int per = (KT + NW - 1) / NW;
     const int k0 = min(wave * per, KT), n = min(per, KT - k0);
     __amdgpu_buffer_rsrc_t dw[R], ds[R], dz[R];
-    bool has_z[R];
+    uint32_t z_fill[R];                           // added to what was read: 0, or 8 for every group
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int m = PAIR ? r / RM : seg, tile = min(tile0 + r % RM, tiles - 1);
@@ -91,8 +91,8 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
         ds[r] = uniform_rsrc(pick_ptr(c.s, m) + at * 16 * SUB, n * 32 * SUB);
         if constexpr (ZP) {
             const uint8_t* z = pick_ptr(c.z, m);
-            has_z[r] = z != nullptr;
-            dz[r] = uniform_rsrc(z + (has_z[r] ? at * 16 * SUB : 0), has_z[r] ? n * 16 * SUB : 0);
+            z_fill[r] = z ? 0u : 0x08080808u;
+            dz[r] = uniform_rsrc(z ? z + at * 16 * SUB : nullptr, z ? n * 16 * SUB : 0);
         }
     }
     const int last = K / 32 - 1;                  // the last slice of 32 inputs
@@ -108,8 +108,9 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
         for (int r = 0; r < R; ++r) {
             w[d][r] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(dw[r], i * kW4Block + lane * 16, 0, kAux));
             s[d][r].load(ds[r], (i * 16 + col) * 2 * SUB, 0);
-            if constexpr (ZP) z[d][r] = has_z[r] ? w4_zeros<SUB>(dz[r], (i * 16 + col) * SUB, 0) : 0x08080808u;
+            if constexpr (ZP) z[d][r] = w4_zeros<SUB>(dz[r], (i * 16 + col) * SUB, 0);   // without zero points: 0
         }
+        __builtin_amdgcn_sched_barrier(0);        // the weights first: they come from HBM
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
                 for (int mt = 0; mt < MT; ++mt) {
                     acc[mt] = c0[mt];
                     if constexpr (ZP) {
-                        const float zf = (float)((z[d][r] >> (8 * g)) & 255u);
+                        const float zf = (float)(((again(z[d][r]) + z_fill[r]) >> (8 * g)) & 255u);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[mt][i] *= zf;
                     }
@@ -147,12 +148,16 @@ __global__ __launch_bounds__(NW * 64) void w4_stream_kernel(W4Call c, int KT, in
 #pragma unroll
                         for (int p = 0; p < P; ++p) acc[mt] = mfma_bf16(a[d][mt][p][g * SL + j], b, acc[mt]);
                 }
-                const float sf = s[d][r].at(g);
+                W4Scales<SUB> t = s[d][r];
+                if constexpr (SUB > 1) t.v[g >> 1] = again(t.v[g >> 1]);
+                const float sf = t.at(g);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tot[r][mt][i] = __builtin_fmaf(sf, acc[mt][i], tot[r][mt][i]);
             }
+            // one group at a time: else the start values of all of them take registers at once
+            if constexpr (SUB > 1) __builtin_amdgcn_sched_barrier(0);
         }
     };
     // one loop exit: with one after every block the compiler waits for every
@@ -320,7 +325,7 @@ hipError_t run(const W4Call& c, hipStream_t st) {
 
 template <int G, bool PAIR, bool EXPERTS>
 hipError_t by_form(int form, const W4Call& c, hipStream_t st) {
-    constexpr int D4 = G == 128 ? 2 : 1;   // two blocks of four row tiles: too many registers with more scales
+    constexpr int D4 = 2;   // two blocks of four row tiles: too many registers with more scales
     if constexpr (!PAIR)
         if (form == kW4Stream16x1) return run<G, kW4Stream16x1, 8, 2, PAIR, EXPERTS>(c, st);
     if (form <= kW4Stream16x2) return run<G, kW4Stream16x2, 8, 2, PAIR, EXPERTS>(c, st);

@@ -17,13 +17,6 @@ namespace qlin {
 
 namespace {
 
-// The same value, unpacked anew at every use: held unpacked for the whole
-// block, the scales and zero points would take the registers of the sums.
-__device__ __forceinline__ uint32_t again(uint32_t v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-
 constexpr int kPanelGroup = 8;   // panels that take turns on the same rows of x (their weights stay in the XCD's L2)
 
 constexpr int kItemGroup = 4;    // items that take turns on the same panel
@@ -105,7 +98,7 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
     const int tile0 = (panel * 4 + wave) * RM;
     const int first = min(tile0, tiles - 1), last = min(RM, tiles - first) - 1;
     __amdgpu_buffer_rsrc_t dw[NM], ds[NM], dz[NM];
-    bool has_z[NM];
+    uint32_t z_fill[NM];         // added to what was read: 0, or 8 for every group
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
         const int64_t at = ((int64_t)e * tiles + first) * KT;
@@ -115,8 +108,8 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
         ds[m] = uniform_rsrc(pick_ptr(c.s, i) + at * 16 * SUB, blocks * 32 * SUB);
         if constexpr (ZP) {
             const uint8_t* z = pick_ptr(c.z, i);
-            has_z[m] = z != nullptr;
-            dz[m] = uniform_rsrc(z + (has_z[m] ? at * 16 * SUB : 0), has_z[m] ? blocks * 16 * SUB : 0);
+            z_fill[m] = z ? 0u : 0x08080808u;
+            dz[m] = uniform_rsrc(z ? z + at * 16 * SUB : nullptr, z ? blocks * 16 * SUB : 0);
         }
     }
 
@@ -137,7 +130,7 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
             const int m = r / RM, b = min(r % RM, last) * KT + kb;
             w[r] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(dw[m], lane * 16, b * kW4Block, 0));
             sn[r].load(ds[m], col * 2 * SUB, b * 32 * SUB);
-            if constexpr (ZP) zn[r] = has_z[m] ? w4_zeros<SUB>(dz[m], col * SUB, b * 16 * SUB) : 0x08080808u;
+            if constexpr (ZP) zn[r] = w4_zeros<SUB>(dz[m], col * SUB, b * 16 * SUB);   // without zero points: 0
         }
     };
     auto x_at = [&](const uint8_t* xs, int mt, int j) {
@@ -207,7 +200,7 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
             for (int j = 0; j < 4; ++j) codes[r][j] = w4_codes(w[r][j]);
             s[r] = sn[r];
             if (i >= nb) s[r] = W4Scales<SUB>{};   // steps past the share add nothing
-            z[r] = zn[r];
+            if constexpr (ZP) z[r] = zn[r] + z_fill[r / RM];
         }
         __builtin_amdgcn_sched_barrier(0);
         load_w(next);
