@@ -63,7 +63,7 @@ struct FormCost {
     double first, more;
 };
 constexpr FormCost kCost128[qlin::kW4Forms] = {{4.0, 3.8}, {4.5, 4.5}, {6.0, 5.8}, {5.9, 5.6}, {10.2, 10.2}, {27, 29}, {44, 68}};
-constexpr FormCost kCost32[qlin::kW4Forms] = {{5.0, 4.6}, {6.5, 6.6}, {8.0, 8.5}, {11, 7.7}, {12.5, 13}, {46, 37}, {95, 128}};
+constexpr FormCost kCost32[qlin::kW4Forms] = {{4.5, 4.3}, {5.5, 5.2}, {9.3, 7.8}, {10, 7.4}, {13.6, 14.5}, {44, 37}, {92, 126}};
 
 double form_cost(int form, const qlin::W4Call& c, bool pair, int64_t blocks) {
     const double w = (double)(blocks * qlin::w4_units(form, c, pair)) / 256.0;
