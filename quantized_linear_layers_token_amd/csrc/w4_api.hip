@@ -244,7 +244,23 @@ namespace {
 struct Workspace {
     int64_t order, items, nitems, h, rows, bytes;
 };
-constexpr int64_t kDirectSlots = 32;     // routed rows that are multiplied one by one, without sorting
+// Few tokens: multiply each slot by its own expert's weights, with no sorting
+// and the weighted sum inside the down product (two launches), or sort the slots
+// by expert and read the weights of each expert once (four)?  Estimates in us.
+// Direct: one round of the 256 CUs per 256 / (H / 16) tokens, which each take the
+// k * I / 128 blocks of a row tile with 16 wavefronts.  Sorted: the launches, and
+// the expected number of different experts times their bytes at 5.2 TB/s.
+// Measured on both sides: 64 experts of 2048 x 1024, 8 choices, 1, 4 and 16
+// tokens: direct 13.1, 27.8, 92, sorted 18.9, 26.8, 46; 8 such experts, 2 choices,
+// 2, 4 and 16 tokens: 12.1, 18.7, 57 and 15.8, 17.7, 19.7; 16 experts of
+// 1024 x 512, 2 choices, 1, 8 and 16 tokens: 8.7, 13, 21 and 13.8, 16, 16.3.
+bool direct_is_faster(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+    const int64_t groups = T * qlin::w4_row_tiles(H);
+    if (groups >= (int64_t(1) << 22)) return false;   // 1024 threads each, below 2^32 of one launch
+    const double direct = 5.5 + std::ceil((double)groups / 256.0) * (4.0 + 1.5 * (double)(k * qlin::w4_k_tiles(I)) / 16.0);
+    const double different = (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)(T * k)));
+    return direct < 13.5 + different * 1.55 * (double)H * (double)I / 5.2e6;
+}
 
 // Items of at most `rows` rows that the routed rows of E experts can need.
 int64_t max_items(int64_t slots, int64_t E, int rows) { return (slots < E ? slots : E) + slots / rows; }
@@ -252,14 +268,14 @@ int64_t max_items(int64_t slots, int64_t E, int rows) { return (slots < E ? slot
 Workspace layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     const int64_t slots = T * k;
     auto pad = [](int64_t b) { return (b + 255) & ~int64_t(255); };
+    // laid out alike whether the slots are sorted or not: the size grows with T
     Workspace w{};
-    const bool direct = slots <= kDirectSlots;
     w.order = 0;
-    w.items = w.order + (direct ? 0 : pad(4 * slots));
-    w.nitems = w.items + (direct ? 0 : pad(12 * max_items(slots, E, 16)));
-    w.h = w.nitems + (direct ? 0 : 256);
+    w.items = w.order + pad(4 * slots);
+    w.nitems = w.items + pad(12 * max_items(slots, E, 16));
+    w.h = w.nitems + 256;
     w.rows = w.h + pad(4 * slots * I);   // two bf16 parts
-    w.bytes = w.rows + (direct ? 0 : pad(4 * slots * H));
+    w.bytes = w.rows + pad(4 * slots * H);
     return w;
 }
 
@@ -306,7 +322,7 @@ qlin_status qlin_experts_w4(const uint16_t* x, int64_t T, int64_t H, int64_t I, 
             return QLIN_ERR_ALIAS;
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool direct = slots <= kDirectSlots;
+    const bool direct = direct_is_faster(T, k, E, H, I);
     int* order = reinterpret_cast<int*>(ws + l.order);
     int* items = reinterpret_cast<int*>(ws + l.items);
     int* nitems = reinterpret_cast<int*>(ws + l.nitems);

@@ -156,6 +156,9 @@ assert experts(work=at(2, -64)) == ALIAS
 assert lib.qlin_experts_w4_workspace(8, 4, 16, 250, 128) == 0 and lib.qlin_experts_w4_workspace(0, 4, 16, 256, 128) == 0
 assert lib.qlin_experts_w4_workspace(8, 4, 16, 256, 128) >= 8 * 4 * 128 * 4
 
+sizes = [lib.qlin_experts_w4_workspace(T, 2, 16, 1024, 512) for T in range(1, 200)]
+assert sizes == sorted(sizes)                            # a workspace serves any fewer tokens
+
 # ---- the choice of forms: 16 x 1, 16 x 2, 16 x 4 (eight or four wavefronts), 32 x 4, tiled 64 x 8, 64 x 16 ----
 big = lambda n: (at(1), at(2), None, n)  # noqa: E731
 for M, N, K, form in [(1, 4096, 4096, 0), (1, 14336, 4096, 3), (32, 4096, 4096, 1), (64, 4096, 4096, 3), (128, 4096, 4096, 4),
