@@ -125,7 +125,7 @@ qlin_status qlin_route(const void* logits, qlin_out logits_type, int64_t T, int6
                        const float* bias, int32_t groups, int32_t top_groups, int32_t group_best, int32_t renormalize,
                        float scale, int32_t* ids, float* weights, hipStream_t stream);
 
-/* Bytes of the workspace of qlin_experts_w4 (0 for sizes out of range).  They
+/* Bytes of the workspace of qlin_experts_w4 (0 for sizes out of range and for no tokens).  They
  * grow with T: a workspace for T tokens serves any fewer. */
 int64_t qlin_experts_w4_workspace(int64_t T, int32_t k, int64_t E, int64_t H, int64_t I);
 

@@ -290,7 +290,7 @@ bool experts_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
 extern "C" {
 
 int64_t qlin_experts_w4_workspace(int64_t T, int32_t k, int64_t E, int64_t H, int64_t I) {
-    if (!experts_sizes(T, k, E, H, I)) return 0;
+    if (!experts_sizes(T, k, E, H, I) || T == 0) return 0;   // no tokens: nothing is launched
     return layout(T, k, E, H, I).bytes;
 }
 
