@@ -19,7 +19,7 @@
  *    f32 per group, scaled in f32 and added in f32.
  *  - Results do not depend on what else runs: the same call gives the same bits.
  *  - A row of x with an infinity or NaN, or with values past 2^112 in magnitude
- *    (whose sums leave f32), gives values that are not finite, or unspecified, in
+ *    (whose sums, or the experts' h, leave f32), gives values that are not finite, or unspecified, in
  *    its own rows of the result and nowhere else.
  */
 #ifndef QLIN_W4_H_

@@ -322,7 +322,6 @@ qlin_status qlin_experts_w4(const uint16_t* x, int64_t T, int64_t H, int64_t I, 
             return QLIN_ERR_ALIAS;
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool direct = direct_is_faster(T, k, E, H, I);
     int* order = reinterpret_cast<int*>(ws + l.order);
     int* items = reinterpret_cast<int*>(ws + l.items);
     int* nitems = reinterpret_cast<int*>(ws + l.nitems);
@@ -354,9 +353,10 @@ qlin_status qlin_experts_w4(const uint16_t* x, int64_t T, int64_t H, int64_t I, 
     b.mode = QLIN_OUT_F32;
     b.K = I;
     b.xdiv = 1;
-    if (direct) {
-        a.max_items = b.max_items = slots;
-        const hipError_t e = product(choose_form(a, true, true, 16), a, true, true, stream);
+    a.max_items = b.max_items = slots;
+    const int one_by_one = direct_is_faster(T, k, E, H, I) ? choose_form(a, true, true, 16) : -1;
+    if (one_by_one >= 0) {
+        const hipError_t e = product(one_by_one, a, true, true, stream);
         if (e != hipSuccess) return qlin::hip_status(e);
         return qlin::hip_status(qlin::launch_experts_down_direct(b, weights, T, k, y, stream));
     }
