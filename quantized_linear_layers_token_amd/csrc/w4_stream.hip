@@ -12,6 +12,8 @@
 // so the sums of x that the zero points need are a product with a constant
 // operand: of -8 where there are no zero points, and its result is then the
 // start value of every tile's sum.  Groups are summed in f32 and scaled in f32.
+// One token, 2 x 14336 x 4096: 12.5 us, 4.8 TB/s (a large copy's rate); 4096 x
+// 4096: 4.4 us, where an empty kernel takes 2.8.
 #include "w4_device.h"
 
 namespace qlin {
@@ -220,7 +222,8 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT,
 // (slot, 128-input block) pairs, so that a single token still keeps every load
 // of its 16 rows in flight, and no row of a slot passes through memory.  The
 // operand's 16 rows are the two parts of h in turn: the sums of rows 0 and 1
-// are those of one part each.
+// are those of one part each.  Eight slots of 2048 x 1024: 8.0 us (7.1 at
+// best, 1.2 TB/s: one round of workgroups, so the latency of its loads bounds it).
 template <int G, int NW, bool ZP>
 __global__ __launch_bounds__(NW * 64) void w4_down_direct_kernel(W4Call c, int KT, int units, const float* __restrict__ weights,
                                                                  int k, uint16_t* __restrict__ y) {

@@ -10,7 +10,10 @@
 // copied there in operand order without passing through registers, so that a
 // read is 16 contiguous bytes per lane.  The sums of x that the zero points
 // need are products with a constant operand, MT / 4 per wavefront and slice,
-// shared through LDS.
+// shared through LDS.  2048 x 4096 x 14336: 241 us, 1.0 PFLOP/s, the matrix
+// cores busy for half of the cycles at the 1.8 GHz that their power allows (the
+// library's bf16 product of that shape: 224 us); 64 experts of 2048 x 1024 with
+// 16384 rows: 187 us for gate and up, 117 for down.
 #include "w4_device.h"
 
 namespace qlin {
