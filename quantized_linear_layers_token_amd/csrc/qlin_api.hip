@@ -4,6 +4,7 @@
 
 #include "../../include/qlin.h"
 #include "qlin_internal.h"
+#include "w4_internal.h"
 
 namespace {
 thread_local int g_last_hip_error = 0;

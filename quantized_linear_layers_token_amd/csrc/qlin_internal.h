@@ -124,9 +124,6 @@ constexpr int64_t kWeightOnlyRowMaxK = 16384;   // one-token kernel keeps the bf
 hipError_t launch_weight_only(int variant, const uint16_t* x, int64_t M, int64_t K, const SegmentArgs& sa, int mode,
                               hipStream_t st);
 
-// The status of a launch; records the HIP error for qlin_last_hip_error.
-qlin_status hip_status(hipError_t e);
-
 int gemv_rows_per_wave(int64_t N, int64_t K);
 
 // qlin_linear with its arguments: validation, then the launch form the call

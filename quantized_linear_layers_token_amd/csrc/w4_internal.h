@@ -10,6 +10,9 @@
 
 namespace qlin {
 
+// The status of a launch; records the HIP error for qlin_last_hip_error (qlin_api.hip).
+qlin_status hip_status(hipError_t e);
+
 // Packed 4-bit weights: one matrix [N, K] is ceil(N / 16) row tiles, each
 // ceil(K / 128) blocks of 1 KiB (16 rows x 128 inputs), see qlin_pack_w4.
 constexpr int kW4Rows = 16;

@@ -1,6 +1,8 @@
 """The 4-bit, routing and experts entry points without a GPU: the header, the exported symbols and the binding agree;
 the C-ABI layer under host sanitizers; the binding's own checks; and the matrix-core result hazard in the new kernels'
 assembly."""
+import hashlib
+import json
 import os
 import re
 import shutil
@@ -136,3 +138,13 @@ def test_every_mfma_result_access_is_padded(tmp_path):
         assert not bad, f"{src}: {bad[:5]}"
         spills = [int(v) for v in re.findall(r"\.vgpr_spill_count:\s+(\d+)", text)]
         assert max(spills) <= 16, f"{src}: {max(spills)} registers spilled"
+
+
+def test_measured_traffic_still_belongs_to_its_sources():
+    """The bench reports the measured bytes of the decode launch only while the sources they belong to are unchanged:
+    what the 4-bit calls need is declared apart from them."""
+    with open(os.path.join(ROOT, "profiles", "linear_decode_int8_llama8b_traffic.json")) as f:
+        recorded = json.load(f)["sources_sha256"]
+    for name, sha in recorded.items():
+        with open(os.path.join(ROOT, "quantized_linear_layers_token_amd", "csrc", name), "rb") as f:
+            assert hashlib.sha256(f.read()).hexdigest() == sha, name
