@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqlin.so")
@@ -373,13 +374,16 @@ class W4Weight:
         self.packed, self.scales, self.zeros = packed, scales, zeros
         self.experts, self.N, self.K, self.group = experts, N, K, group
         self.device = packed.device
-        self._struct = QlinW4Weight(packed.data_ptr(), scales.data_ptr(), _ptr(zeros), N)
-        self._ref = ctypes.byref(self._struct)
+        # struct qlin_w4_weight as bytes: arrays of them are joined without building a ctypes object for each call
+        self._bytes = bytes(QlinW4Weight(packed.data_ptr(), scales.data_ptr(), _ptr(zeros), N))
 
 
 # Handle of a device's current stream, without building a Stream object where torch offers that.
 _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream",
                       lambda index: _torch.cuda.current_stream(index).cuda_stream)
+
+
+_current_device = getattr(_torch._C, "_cuda_getDevice", _torch.cuda.current_device)
 
 
 def _launch(fn, device, stream, *args):
@@ -390,7 +394,7 @@ def _launch(fn, device, stream, *args):
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if index == _torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, stream)
     else:
         with _torch.cuda.device(index):
@@ -399,13 +403,18 @@ def _launch(fn, device, stream, *args):
         raise QlinError(status, fn.__name__)
 
 
+# Types by element size; float16 is no type of theirs.
+_TYPES = {size: frozenset(t for t in vars(_torch).values()
+                          if isinstance(t, _torch.dtype) and t.itemsize == size and t is not _torch.float16) for size in (1, 2, 4)}
+
+
 def _w4_tensor(t, name, shape, size, device):
     """One tensor argument of the calls below: exactly this shape (None: any), contiguous, on the call's device."""
-    if t.element_size() != size or (shape is not None and t.shape != shape) or not t.is_contiguous():
+    if t.dtype not in _TYPES[size] or (shape is not None and t.shape != shape) or not t.is_contiguous():
+        if t.dtype is _torch.float16:
+            raise ValueError(f"{name} must be bfloat16 (or its bit patterns), not float16")
         raise ValueError(f"{name} must be a contiguous tensor of {size}-byte elements"
                          + (f" and shape {list(shape)}, not {list(t.shape)}" if shape is not None else ""))
-    if t.dtype is _torch.float16:
-        raise ValueError(f"{name} must be bfloat16 (or its bit patterns), not float16")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
 
@@ -437,14 +446,19 @@ def qlin_pack_w4(q_w, s_w, z_w=None):
     return W4Weight(packed, scales, zeros, E, N, K, group)
 
 
-def _w4_input(x, w, name):
-    if x.dim() != 2 or x.element_size() != 2 or not x.is_contiguous() or x.dtype is _torch.float16:
+def _w4_input(x):
+    """-> (device, M, K) of the activations."""
+    if x.dtype not in _TYPES[2] or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D tensor of bfloat16 (or its bit patterns)")
-    if w.K != x.shape[1] or w.device != x.device:
-        raise ValueError(f"{name} has {w.K} inputs on {w.device}, x {x.shape[1]} on {x.device}")
+    return x.device, *x.shape
 
 
-_W4_ARRAYS = [(QlinW4Weight * n, _P * n) for n in range(MAX_SEGMENTS + 1)]
+def _w4_reads(w, name, K, device):
+    if w.K != K or w.device != device:
+        raise ValueError(f"{name} has {w.K} inputs on {w.device}, x {K} on {device}")
+
+
+_POINTERS = [struct.Struct(f"{n}Q").pack for n in range(MAX_SEGMENTS + 1)]
 
 
 def qlin_linear_w4(x, segments, out=OUT_BF16, stream=None):
@@ -452,50 +466,47 @@ def qlin_linear_w4(x, segments, out=OUT_BF16, stream=None):
     nw = len(segments)
     if not 1 <= nw <= MAX_SEGMENTS:
         raise ValueError(f"segments must hold one to {MAX_SEGMENTS} (weight, y) pairs")
-    device, (M, K), group, size = x.device, x.shape, segments[0][0].group, _out_bytes(out)
+    device, M, K = _w4_input(x)
+    group, size = segments[0][0].group, _out_bytes(out)
     for w, y in segments:
-        _w4_input(x, w, "a segment")
+        _w4_reads(w, "a segment", K, device)
         if w.experts != 1 or w.group != group:
             raise ValueError("every segment must be one matrix, all of one group size")
         _w4_tensor(y, "a segment's y", (M, w.N), size, device)
-    if nw == 1:
-        weights, ys = w._ref, ctypes.byref(_P(y.data_ptr()))
-    else:
-        weight_array, pointer_array = _W4_ARRAYS[nw]
-        weights = weight_array(*[w._struct for w, _ in segments])
-        ys = pointer_array(*[y.data_ptr() for _, y in segments])
-    _launch(_lib.qlin_linear_w4, device, stream, x.data_ptr(), M, K, group, weights, ys, nw, out)
+    weights = w._bytes if nw == 1 else b"".join([w._bytes for w, _ in segments])
+    _launch(_lib.qlin_linear_w4, device, stream, x.data_ptr(), M, K, group, weights,
+            _POINTERS[nw](*[y.data_ptr() for _, y in segments]), nw, out)
 
 
 def qlin_linear_swiglu_w4(x, gate, up, h, stream=None):
     """x bf16 [M, K]; gate, up: W4Weight [I, K]; h bf16 [M, I] receives silu(x gate^T) * (x up^T), rounded once."""
-    _w4_input(x, gate, "gate")
-    _w4_input(x, up, "up")
-    M, K = x.shape
+    device, M, K = _w4_input(x)
+    _w4_reads(gate, "gate", K, device)
+    _w4_reads(up, "up", K, device)
     if gate.experts != 1 or up.experts != 1 or gate.N != up.N or gate.group != up.group:
         raise ValueError("gate and up must be one matrix each, of one shape and group size")
-    _w4_tensor(h, "h", (M, gate.N), 2, x.device)
-    _launch(_lib.qlin_linear_swiglu_w4, x.device, stream, x.data_ptr(), M, K, gate.group, gate._ref, up._ref, h.data_ptr())
+    _w4_tensor(h, "h", (M, gate.N), 2, device)
+    _launch(_lib.qlin_linear_swiglu_w4, device, stream, x.data_ptr(), M, K, gate.group, gate._bytes, up._bytes, h.data_ptr())
 
 
 def qlin_route(logits, ids, weights, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, group_best=2,
                renormalize=True, scale=1.0, stream=None):
     """logits bf16 or f32 [T, E]; ids int32 [T, k] and weights f32 [T, k] receive the k experts of each token."""
-    if logits.dim() != 2 or not logits.is_contiguous() or logits.dtype not in (_torch.bfloat16, _torch.float32):
+    dtype, device = logits.dtype, logits.device
+    if (dtype is not _torch.float32 and dtype is not _torch.bfloat16) or logits.dim() != 2 or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous 2-D tensor of bfloat16 or float32")
     T, E = logits.shape
-    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != _torch.int32 or weights.dtype != _torch.float32:
+    if ids.dtype is not _torch.int32 or weights.dtype is not _torch.float32 or ids.dim() != 2:
         raise ValueError("ids must be int32 [T, k] and weights float32 [T, k]")
-    k = ids.shape[1]
-    _w4_tensor(ids, "ids", None, 4, logits.device)
-    _w4_tensor(weights, "weights", (T, k), 4, logits.device)
+    shape = (T, ids.shape[1])
+    _w4_tensor(ids, "ids", shape, 4, device)
+    _w4_tensor(weights, "weights", shape, 4, device)
     if bias is not None:
-        if bias.dtype != _torch.float32:
+        if bias.dtype is not _torch.float32:
             raise ValueError("bias must be float32 [E]")
-        _w4_tensor(bias, "bias", (E,), 4, logits.device)
-    _launch(_lib.qlin_route, logits.device, stream, logits.data_ptr(), OUT_F32 if logits.dtype == _torch.float32 else OUT_BF16, T, E,
-            k, score, _ptr(bias), groups, top_groups, group_best, 1 if renormalize else 0, scale, ids.data_ptr(),
-            weights.data_ptr())
+        _w4_tensor(bias, "bias", (E,), 4, device)
+    _launch(_lib.qlin_route, device, stream, logits.data_ptr(), OUT_F32 if dtype is _torch.float32 else OUT_BF16, T, E, shape[1],
+            score, _ptr(bias), groups, top_groups, group_best, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr())
 
 
 def qlin_experts_w4_workspace(T, k, gate, up, down):
@@ -509,17 +520,16 @@ def qlin_experts_w4_workspace(T, k, gate, up, down):
 def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
     """x bf16 [T, H]; ids int32 [T, k] (outside 0..E-1: no expert), weights f32 [T, k]; gate, up: W4Weight of E
     matrices [I, H], down of E matrices [H, I]; y bf16 [T, H]; workspace uint8, qlin_experts_w4_workspace bytes."""
-    _w4_input(x, gate, "gate")
-    T, H = x.shape
+    device, T, H = _w4_input(x)
+    _w4_reads(gate, "gate", H, device)
     E, I, group = gate.experts, gate.N, gate.group
     if (up.experts, up.N, up.K, up.group) != (E, I, H, group) or (down.experts, down.N, down.K, down.group) != (E, H, I, group):
         raise ValueError("up must have gate's shape, down be [E, H, I], all of one group size")
-    if up.device != x.device or down.device != x.device:
-        raise ValueError(f"every tensor must be on {x.device}")
+    if up.device != device or down.device != device:
+        raise ValueError(f"every tensor must be on {device}")
     if ids.dim() != 2 or ids.dtype != _torch.int32 or weights.dtype != _torch.float32:
         raise ValueError("ids must be int32 [T, k] and weights float32 [T, k]")
     k = ids.shape[1]
-    device = x.device
     _w4_tensor(ids, "ids", (T, k), 4, device)
     _w4_tensor(weights, "weights", (T, k), 4, device)
     _w4_tensor(y, "y", (T, H), 2, device)
@@ -528,4 +538,4 @@ def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
     if workspace.numel() < need:
         raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
     _launch(_lib.qlin_experts_w4, device, stream, x.data_ptr(), T, H, I, E, k, group, ids.data_ptr(), weights.data_ptr(),
-            gate._ref, up._ref, down._ref, y.data_ptr(), workspace.data_ptr())
+            gate._bytes, up._bytes, down._bytes, y.data_ptr(), workspace.data_ptr())
