@@ -244,22 +244,29 @@ namespace {
 struct Workspace {
     int64_t order, items, nitems, h, rows, bytes;
 };
+// Few ids: the workgroups of gate and up find the rows of their item themselves
+// (w4_stream.hip), with no launch for the sorting: 37 tokens of 6 choices among
+// 40 experts 43.4 -> 40.5 us, 16 tokens of 2 among 8: 18.8 -> 15.6.
+bool own_items(int64_t slots, int64_t E) { return slots <= qlin::kOwnItemSlots && E <= qlin::kOwnItemExperts; }
 // Few tokens: multiply each slot by its own expert's weights, with no sorting
 // and the weighted sum inside the down product (two launches), or sort the slots
-// by expert and read the weights of each expert once (four)?  Estimates in us.
-// Direct: one round of the 256 CUs per 256 / (H / 16) tokens, which each take the
-// k * I / 128 blocks of a row tile with 16 wavefronts.  Sorted: the launches, and
-// the expected number of different experts times their bytes at 5.2 TB/s.
-// Measured on both sides: 64 experts of 2048 x 1024, 8 choices, 1, 4 and 16
-// tokens: direct 13.1, 27.8, 92, sorted 18.9, 26.8, 46; 8 such experts, 2 choices,
-// 2, 4 and 16 tokens: 12.1, 18.7, 57 and 15.8, 17.7, 19.7; 16 experts of
-// 1024 x 512, 2 choices, 1, 8 and 16 tokens: 8.7, 13, 21 and 13.8, 16, 16.3.
+// by expert and read the weights of each expert once (three or four)?  Estimates
+// in us.  Direct: one round of the 256 CUs per 256 / (H / 16) tokens, which each
+// take the k * I / 128 blocks of a row tile with 16 wavefronts (half a round or
+// less takes three quarters of one).  Sorted: the launches, and the expected
+// number of different experts times their bytes at 5.6 TB/s.  Measured, direct
+// and sorted: 64 experts of 2048 x 1024, 8 choices, 1, 2, 4 and 8 tokens: 13.7 and
+// 16.1, 17.8 and 21.2, 30.0 and 28.6, 52 and 37; 8 such experts, 2 choices, 2, 4
+// and 8 tokens: 11.8 and 12.4, 19.2 and 14.8, 31 and 14.9; 16 experts of
+// 1024 x 512, 2 choices, 4, 8 and 16 tokens: 9.0 and 11.6, 13.3 and 12.4, 20.9 and
+// 12.9; 300 of 512 x 256, 4 choices, 8 tokens: 9.7 and 19.1.
 bool direct_is_faster(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     const int64_t groups = T * qlin::w4_row_tiles(H);
     if (groups >= (int64_t(1) << 22)) return false;   // 1024 threads each, below 2^32 of one launch
-    const double direct = 5.5 + std::ceil((double)groups / 256.0) * (4.0 + 1.5 * (double)(k * qlin::w4_k_tiles(I)) / 16.0);
+    const double rounds = groups <= 128 ? 0.75 : std::ceil((double)groups / 256.0);
+    const double direct = 5.5 + rounds * (4.0 + 1.5 * (double)(k * qlin::w4_k_tiles(I)) / 16.0);
     const double different = (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)(T * k)));
-    return direct < 13.5 + different * 1.55 * (double)H * (double)I / 5.2e6;
+    return direct < (own_items(T * k, E) ? 11.0 : 14.0) + different * 1.4 * (double)H * (double)I / 5.2e6;
 }
 
 // Items of at most `rows` rows that the routed rows of E experts can need.
@@ -378,7 +385,9 @@ qlin_status qlin_experts_w4(const uint16_t* x, int64_t T, int64_t H, int64_t I, 
     a.order = b.order = order;
     a.items = b.items = items;
     a.nitems = b.nitems = nitems;
-    hipError_t e = qlin::launch_experts_plan(ids, slots, (int)E, item_rows, order, items, nitems, stream);
+    hipError_t e = hipSuccess;
+    if (item_rows < 64 && own_items(slots, E)) a.slots = (int)slots;
+    else e = qlin::launch_experts_plan(ids, slots, (int)E, item_rows, order, items, nitems, stream);
     if (e == hipSuccess) e = product(form_a, a, true, true, stream);
     if (e == hipSuccess) e = product(form_b, b, false, true, stream);
     if (e == hipSuccess) e = qlin::launch_experts_combine(rows, ids, weights, T, k, (int)E, H, y, stream);

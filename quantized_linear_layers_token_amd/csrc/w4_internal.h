@@ -39,9 +39,11 @@ struct W4Call {
     int64_t M, K;
     // experts
     const int* ids;                    // expert of each slot (slot = token * k + choice)
-    const int* order;                  // slots in the order of their experts
-    const int* items;                  // {expert, first place in order, rows}; null: item i is slot i alone
-    const int* nitems;
+    int* order;                        // slots in the order of their experts
+    int* items;                        // {expert, first place in order, rows}; null: item i is slot i alone
+    int* nitems;
+    int slots;                         // > 0 (gate/up, streamed): these many ids are not sorted yet: the workgroups find
+                                       // their items themselves and write order, items and nitems
     int E;
     int xdiv;                          // row of x of a slot: slot / xdiv
     int64_t max_items;                 // bound of *nitems (slots where items is null)
@@ -81,6 +83,9 @@ inline int64_t w4_blocks(int form, const W4Call& c, bool experts) {
 hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int k, int score, const float* bias, int groups,
                         int top_groups, int group_best, bool renorm, float scale, int32_t* ids, float* weights,
                         hipStream_t st);
+
+// The streaming forms of gate and up find their items by themselves up to these sizes.
+constexpr int kOwnItemSlots = 512, kOwnItemExperts = 256;
 
 // The routed rows sorted by expert and cut into items of at most block_rows
 // rows of one expert.  order [T * k], items [3 * max_items], nitems [1].

@@ -24,6 +24,79 @@ namespace {
 
 constexpr int kAux = 2;   // buffer-load cache policy: streaming
 
+// Sum over the lanes up to and with this one: shifts by 1, 2, 4, 8 in the rows
+// of 16 lanes, then the last lane of a row added to the rows after it.
+__device__ __forceinline__ int lane_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
+// The item `block` of the ids (rows of one expert, ROWS at most, experts and
+// slots in order), found by one wavefront for itself: the experts counted in
+// `hist` (64 * ceil(E / 64) ints), items and rows summed over the lanes, which
+// own ceil(E / 64) consecutive experts each, and the slots of the item's expert
+// found by ballots, into `list`.  rows = 0: no such item.  total: their number;
+// place: rows before this item.  (About 1 us per workgroup; a launch that sorts
+// costs 3.9 us and three loads in turn to read what it found.  Done again by the
+// second product it gains nothing: that one reads what the first wrote down.)
+template <int ROWS>
+__device__ __forceinline__ void own_item(const int* __restrict__ ids, int slots, int E, int block, int lane, int* hist, int* list,
+                                         int& expert, int& rows, int& place, int& total) {
+    constexpr int B = kOwnItemSlots / 64;
+    const int per = (E + 63) >> 6;
+    int id[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) id[b] = b * 64 + lane < slots ? ids[b * 64 + lane] : -1;
+    for (int p = 0; p < per; ++p) hist[p * 64 + lane] = 0;
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+        if ((unsigned)id[b] < (unsigned)E) atomicAdd(&hist[id[b]], 1);
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+    int mine = 0;                         // items in the upper half, rows in the lower
+    for (int p = 0; p < per; ++p) {
+        const int n = hist[lane * per + p];
+        mine += ((n + ROWS - 1) / ROWS << 16) + n;
+    }
+    const int upto = lane_scan(mine);
+    const uint64_t past = __ballot((upto >> 16) > block);
+    total = __builtin_amdgcn_readlane(upto, 63) >> 16;
+    rows = expert = place = 0;
+    if (past == 0) return;
+    const int who = __builtin_ctzll(past);
+    const int before = __builtin_amdgcn_readlane(upto - mine, who);
+    int base = before >> 16, count = 0;
+    place = before & 0xFFFF;
+    for (int p = 0; p < per; ++p) {       // (ends at the item's expert: it is one of this lane's)
+        expert = who * per + p;
+        count = __builtin_amdgcn_readfirstlane(hist[expert]);
+        const int items = (count + ROWS - 1) / ROWS;
+        if (block < base + items) break;
+        base += items;
+        place += count;
+    }
+    const int begin = (block - base) * ROWS;
+    place += begin;
+    rows = min(ROWS, count - begin);
+    int seen = -begin;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        const uint64_t same = __ballot(id[b] == expert);
+        const int at = seen + __popcll(same & ((uint64_t(1) << lane) - 1));
+        if (id[b] == expert && at >= 0 && at < ROWS) list[at] = b * 64 + lane;
+        seen += __popcll(same);
+    }
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+}
+
 // D: blocks of 128 inputs whose loads are in flight per wavefront.
 template <int G, int MT, int R, int NW, int D, bool ZP, bool PAIR, bool EXPERTS>
 __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT, int units, int units0, int units1, int units2) {
@@ -33,6 +106,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT,
     constexpr int RM = PAIR ? R / 2 : R;          // row tiles of each matrix
     constexpr int P = EXPERTS && !PAIR ? 2 : 1;   // bf16 parts of an input (the experts' h comes in two)
     __shared__ __attribute__((aligned(16))) float red[NW * R * T * 16];
+    __shared__ int own[PAIR && EXPERTS ? NW : 1][T];   // the rows of an item that the wavefronts found
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -56,7 +130,20 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT,
     int e = 0, begin = 0, rows;
     int64_t m0 = 0;
     if constexpr (EXPERTS) {
-        if (c.items) {
+        if (PAIR && c.slots > 0) {
+            // counted in this wavefront's part of `red`, which it writes only at the end; those of the
+            // first row tiles write the item down for the second product
+            static_assert(R * T * 16 >= kOwnItemExperts, "counts fit the wavefront's sums");
+            int total;
+            own_item<T>(c.ids, c.slots, c.E, block, lane, reinterpret_cast<int*>(red) + wave * (R * T * 16), own[wave], e, rows, begin,
+                        total);
+            if (unit == 0 && wave == 0) {
+                if (block == 0 && lane == 0) *c.nitems = total;
+                if (rows > 0 && lane < 3) c.items[3 * block + lane] = lane == 0 ? e : lane == 1 ? begin : rows;
+                if (lane < rows) c.order[begin + lane] = own[0][lane];
+            }
+            if (rows == 0) return;
+        } else if (c.items) {
             if (block >= *c.nitems) return;
             e = c.items[3 * block];
             begin = c.items[3 * block + 1];
@@ -71,7 +158,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT,
         rows = (int)min((int64_t)T, c.M - m0);
     }
     auto row_of = [&](int t) -> int64_t {         // output row of the block's row t
-        if constexpr (EXPERTS) return c.items ? (int64_t)c.order[begin + t] : (int64_t)block;
+        if constexpr (EXPERTS) return PAIR && c.slots > 0 ? (int64_t)own[wave][t] : c.items ? (int64_t)c.order[begin + t] : (int64_t)block;
         else return m0 + t;
     };
     Global<uint16_t> xp[MT];

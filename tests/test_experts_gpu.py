@@ -207,3 +207,19 @@ def test_few_rows_keep_16_bits_of_h(T, E, k, H, I, group, zeros):
     y = run(xb, ids, wt, ws)
     ref, bound = R.experts(R.bf16_values(xb), ids, wt, *ws, group, h_half=2.0 ** -16)
     assert (np.abs(y - ref) <= bound + R.BF16_HALF * (np.abs(ref) + bound)).all()
+
+
+@pytest.mark.parametrize("T,E,k,group", [(128, 256, 4, 32), (128, 257, 4, 32), (129, 256, 4, 32), (512, 100, 1, 64), (64, 65, 8, 128),
+                                         (33, 64, 15, 64), (256, 3, 2, 32)])
+def test_around_the_sizes_that_need_no_sorting_launch(T, E, k, group):
+    """Up to 512 slots of up to 256 experts are not sorted by a launch of their own: both sides, with ids that are no
+    expert's, a skewed choice, and an expert chosen by every token."""
+    H, I = 128, 256
+    xb, ids, wt, ws = make(11, T, E, k, H, I, group, False, skew=3.0)
+    rng = np.random.default_rng([12, T, E])
+    ids = np.where(rng.random(ids.shape) < 0.1, rng.choice(np.array([-1, E, -2 ** 31, 2 ** 31 - 1], np.int64), ids.shape),
+                   ids).astype(np.int32)
+    ids[:, 0] = E - 1
+    check(run(xb, ids, wt, ws), xb, ids, wt, ws, group)
+    again = [run(xb, ids, wt, ws) for _ in range(2)]
+    assert np.array_equal(again[0], again[1])
