@@ -1,5 +1,6 @@
-// The experts' MLP around its two products: the routed rows sorted by expert,
-// and the weighted sum of each token's rows.
+// The experts' MLP around its two products: the routed rows sorted by expert
+// (few of them are sorted inside the gate and up product instead), and the
+// weighted sum of each token's rows.
 #include "w4_device.h"
 
 namespace qlin {
