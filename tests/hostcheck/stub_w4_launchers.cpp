@@ -23,6 +23,9 @@ hipError_t product(int form, const qlin::W4Call& c, bool pair, bool experts) {
     g_bad |= groups <= 0 || groups * qlin::kW4FormThreads[form] >= (int64_t(1) << 32);
     g_bad |= experts && tiled && !c.items;            // the tiled kernel goes by items
     g_bad |= pair && form == qlin::kW4Stream16x1;
+    // items found by the workgroups: streamed gate and up only, within the sizes that fit, with room to write them down
+    g_bad |= c.slots > 0 && (!experts || !pair || tiled || !c.items || !c.order || !c.nitems ||
+                             c.slots > qlin::kOwnItemSlots || c.E > qlin::kOwnItemExperts);
     return reached();
 }
 }  // namespace
