@@ -104,8 +104,10 @@ typedef enum qlin_score {
  *   score[e]: softmax or sigmoid of the token's logits;
  *   choice[e] = score[e] + bias[e] (bias f32 [E], or null);
  *   groups > 1: the experts form `groups` runs of E / groups; a run's worth is
- *     the sum of its group_best (1 or 2) largest choices, the top_groups runs of
- *     the largest worth stay and no expert of another run is chosen;
+ *     the sum of the group_best (1 or 2) largest choices of its experts that are
+ *     not masked out (one alone counts alone), the top_groups runs of the largest
+ *     worth stay and no expert of another run is chosen; a run whose experts are
+ *     all masked out comes after every other run;
  *   ids[t, 0..k): the experts with the k largest choices, largest first;
  *   weights[t, j] = scale * score[ids[t, j]], divided by the sum of the token's
  *     k chosen scores if renormalize (0 where that sum is 0).
@@ -113,8 +115,9 @@ typedef enum qlin_score {
  * evaluated in f64, and where the order of the choices is that of the logits
  * (no bias; no groups, or group_best 1) they are compared as logits: the choice
  * does not depend on rounding.  An expert whose logit is -infinity or NaN is
- * masked out: score 0, after every other expert of the runs that stay (in
- * index order, so ids are always k different experts); +infinity counts as the
+ * masked out: score 0, its bias counts for nothing, and it comes after every
+ * other expert of the runs that stay (in index order, so ids are always k
+ * different experts); +infinity counts as the
  * largest finite value, and so do infinite biases (NaN as the smallest).  A token whose
  * experts are all masked out gets weights 0.
  * 1 <= k <= min(QLIN_MAX_CHOICES, top_groups * E / groups), E <= QLIN_MAX_EXPERTS,

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
         if constexpr (SCORES) {
             double v = p[j] * inv;
             if (bias && e < E) v += (double)bias[e];
-            c[j] = l[j] == -INFINITY ? -DBL_MAX : finite(v);
+            c[j] = l[j] == -INFINITY ? -INFINITY : finite(v);   // masked out: below every choice
             // f32 rounding keeps the order; past its range every choice shares the last key
             key[j] = key_of((float)fmax(fmin(c[j], (double)FLT_MAX), -(double)FLT_MAX));
         } else {
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
     if (groups > 1) {
         const int size = E / groups;
 #pragma unroll
-        for (int j = 0; j < V; ++j) mine[j * 64 + lane] = SCORES ? c[SCORES ? j : 0] : l[j] == -INFINITY ? -DBL_MAX : (double)l[j];
+        for (int j = 0; j < V; ++j) mine[j * 64 + lane] = SCORES ? c[SCORES ? j : 0] : (double)l[j];
         __builtin_amdgcn_wave_barrier();
         __threadfence_block();
         // P lanes per group walk its experts and keep the two best
@@ -190,7 +190,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(
             b = fmax(fmin(a, oa), fmax(b, ob));
             a = fmax(a, oa);
         }
-        double worth = group_best == 2 && size > 1 ? finite(a + b) : a;
+        // of the experts that take part: one alone is its group's worth, and a
+        // group without any stays at -infinity, after every other
+        const double worth = group_best == 2 && b != -INFINITY ? finite(a + b) : a;
         // a group stays if fewer than top_groups groups come before it
         int before = 0;
         for (int o = 0; o < groups; ++o) {
