@@ -368,14 +368,20 @@ import torch as _torch  # noqa: E402  (loaded with the library above)
 
 class W4Weight:
     """4-bit weights laid out for the library by qlin_pack_w4: one matrix
-    [N, K], or `experts` of them.  Owns the packed tensors."""
+    [N, K], or `experts` of them.  Owns the packed tensors, which cannot be
+    replaced (their contents can be written); copies and pickles hold tensors of
+    their own."""
 
     def __init__(self, packed, scales, zeros, experts, N, K, group):
-        self.packed, self.scales, self.zeros = packed, scales, zeros
-        self.experts, self.N, self.K, self.group = experts, N, K, group
-        self.device = packed.device
         # struct qlin_w4_weight as bytes: arrays of them are joined without building a ctypes object for each call
-        self._bytes = bytes(QlinW4Weight(packed.data_ptr(), scales.data_ptr(), _ptr(zeros), N))
+        vars(self).update(packed=packed, scales=scales, zeros=zeros, experts=experts, N=N, K=K, group=group, device=packed.device,
+                          _bytes=bytes(QlinW4Weight(packed.data_ptr(), scales.data_ptr(), _ptr(zeros), N)))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of a W4Weight cannot be replaced: pack the weights anew")
+
+    def __reduce__(self):    # built again from the tensors: the addresses are theirs alone
+        return W4Weight, (self.packed, self.scales, self.zeros, self.experts, self.N, self.K, self.group)
 
 
 # Handle of a device's current stream, without building a Stream object where torch offers that.
