@@ -58,7 +58,8 @@ constexpr int64_t kMaxElements = int64_t(1) << 40;
 // 19.6, 12.5, 9.74, 9.69, 13.4, 29.1, 47.3 (16 x 4 with four wavefronts chosen);
 // 512 rows 125, 72, 48, 46, 40, 31.6, 47.6 (64 x 8 chosen); 2048 rows 489, 268,
 // 179, 181, 145, 117, 73.6 (64 x 16 chosen).  Over 130 shapes off these the
-// choice was 5 % slower than the best form, in the geometric mean.
+// choice was 5 % slower than the best form, in the geometric mean.  (16 x 4 by
+// eight wavefronts is not built for groups of 128: its costs there serve the mean.)
 struct FormCost {
     double first, more;
 };
@@ -87,8 +88,8 @@ bool form_fits(int form, const qlin::W4Call& c, bool pair, int64_t blocks) {
 int choose_form(const qlin::W4Call& c, bool pair, bool experts, int rows) {
     int best = -1;
     double least = 0;
-    for (int f = pair ? 1 : 0; f < qlin::kW4Forms; ++f) {
-        if (rows && qlin::kW4FormRows[f] != rows) continue;
+    for (int f = 0; f < qlin::kW4Forms; ++f) {
+        if (!qlin::w4_form_built(f, c.group, pair) || (rows && qlin::kW4FormRows[f] != rows)) continue;
         const int64_t blocks = qlin::w4_blocks(f, c, experts);
         if (!form_fits(f, c, pair, blocks)) continue;
         const double cost = form_cost(f, c, pair, blocks);

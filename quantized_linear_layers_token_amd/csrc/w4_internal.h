@@ -61,6 +61,12 @@ enum W4Form : int { kW4Stream16x1 = 0, kW4Stream16x2, kW4Stream16x4, kW4Stream16
 constexpr int kW4FormRows[kW4Forms] = {16, 16, 16, 16, 32, 64, 64};
 constexpr int kW4FormTiles[kW4Forms] = {1, 2, 4, 4, 4, 8, 16};
 constexpr int kW4FormThreads[kW4Forms] = {512, 512, 512, 256, 512, 512, 256};
+// The forms that the library holds: no row tile for the second matrix of a pair
+// in the first; and with groups of 128, 16 x 4 by eight wavefronts is slower than
+// by four at any size (6.0 / 5.8 against 5.9 / 5.6 in the cost table).
+constexpr bool w4_form_built(int form, int group, bool pair) {
+    return !(form == kW4Stream16x1 && pair) && !(form == kW4Stream16x4 && group == 128);
+}
 
 // y (or, with pair, h = silu(x w[0]^T) * (x w[1]^T)) in the given form.  Between
 // the two products of the experts, the streaming forms write and read h as two

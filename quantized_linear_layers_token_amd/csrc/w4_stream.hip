@@ -143,7 +143,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT,
                 if (lane < rows) c.order[begin + lane] = own[0][lane];
             }
             if (rows == 0) return;
-        } else if (c.items) {
+        } else if (!PAIR || c.items) {            // (the down product of single slots is another kernel)
             if (block >= *c.nitems) return;
             e = c.items[3 * block];
             begin = c.items[3 * block + 1];
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Call c, int KT,
         rows = (int)min((int64_t)T, c.M - m0);
     }
     auto row_of = [&](int t) -> int64_t {         // output row of the block's row t
-        if constexpr (EXPERTS) return PAIR && c.slots > 0 ? (int64_t)own[wave][t] : c.items ? (int64_t)c.order[begin + t] : (int64_t)block;
+        if constexpr (EXPERTS) return PAIR && c.slots > 0 ? (int64_t)own[wave][t] : !PAIR || c.items ? (int64_t)c.order[begin + t] : (int64_t)block;
         else return m0 + t;
     };
     Global<uint16_t> xp[MT];
@@ -418,10 +418,11 @@ hipError_t run(const W4Call& c, hipStream_t st) {
 template <int G, bool PAIR, bool EXPERTS>
 hipError_t by_form(int form, const W4Call& c, hipStream_t st) {
     constexpr int D4 = 2;   // two blocks of four row tiles: too many registers with more scales
-    if constexpr (!PAIR)
+    if constexpr (w4_form_built(kW4Stream16x1, G, PAIR))
         if (form == kW4Stream16x1) return run<G, kW4Stream16x1, 8, 2, PAIR, EXPERTS>(c, st);
     if (form <= kW4Stream16x2) return run<G, kW4Stream16x2, 8, 2, PAIR, EXPERTS>(c, st);
-    if (form == kW4Stream16x4) return run<G, kW4Stream16x4, 8, 1, PAIR, EXPERTS>(c, st);
+    if constexpr (w4_form_built(kW4Stream16x4, G, PAIR))
+        if (form == kW4Stream16x4) return run<G, kW4Stream16x4, 8, 1, PAIR, EXPERTS>(c, st);
     if (form == kW4Stream16x4W4) return run<G, kW4Stream16x4W4, 4, D4, PAIR, EXPERTS>(c, st);
     return run<G, kW4Stream32x4, 8, 1, PAIR, EXPERTS>(c, st);
 }
