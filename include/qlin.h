@@ -50,7 +50,7 @@ extern "C" {
 /* Same type as HIP's own hipStream_t. */
 typedef struct ihipStream_t* hipStream_t;
 
-#define QLIN_ABI_VERSION 3
+#define QLIN_ABI_VERSION 4          /* 4: with the calls of qlin_w4.h */
 #define QLIN_MAX_K  131072          /* 127 * 128 * K stays below 2^31 */
 #define QLIN_MAX_MN (1 << 24)
 

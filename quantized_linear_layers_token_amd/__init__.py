@@ -26,7 +26,7 @@ PATH_LARGE_256X128, PATH_LARGE_128X128, PATH_LARGE_128X64, PATH_LARGE_128X256 = 
 PATH_LARGE_128X128_K2, PATH_LARGE_128X64_K2 = 8, 9
 PATH_LARGE_256X256_W8 = 10   # int8 and FP8 rowwise only
 PATH_LARGE_256X256 = 11      # int8 and FP8 rowwise only
-ABI_VERSION = 3
+ABI_VERSION = 4
 NOALLOC_MAX_CODE_BYTES = 16 << 20    # staging capacity of qlin_linear_noalloc
 NOALLOC_MAX_SCALES = 1 << 20
 MAX_K = 131072
@@ -102,12 +102,12 @@ def _load():
             f"{LIB_PATH} is missing: build it with `python quantized_linear_layers_token_amd/build.py` "
             "(the HIP library is the only implementation; there is no fallback)")
     lib = ctypes.CDLL(LIB_PATH)
+    if lib.qlin_abi_version() != ABI_VERSION:      # (int and no arguments: ctypes' default) before a symbol can be missing
+        raise ImportError(f"libqlin ABI {lib.qlin_abi_version()} != binding ABI {ABI_VERSION}")
     for name, (res, args) in {**SIGNATURES, **SIGNATURES_W4}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    if lib.qlin_abi_version() != ABI_VERSION:
-        raise ImportError(f"libqlin ABI {lib.qlin_abi_version()} != binding ABI {ABI_VERSION}")
     return lib
 
 
