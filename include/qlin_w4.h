@@ -12,8 +12,10 @@
  *    per `group` consecutive inputs of a row (group 32, 64 or 128; K a multiple
  *    of it) and either one zero point (uint8) per scale or 8 for all of them:
  *        w[n, k] = (code[n, k] - zero[n, k / group]) * scale[n, k / group]
- *    K is a multiple of 32 and at most QLIN_MAX_K; N is any number up to
- *    QLIN_MAX_MN.
+ *    K is a multiple of 32 and at most QLIN_MAX_K; the rows N of a call's
+ *    matrices (of the two of a gate/up pair together) are any number up to
+ *    QLIN_MAX_MN, its outputs (the experts': T * k rows of the longer of H and I)
+ *    up to 2^40 (QLIN_ERR_SHAPE).
  *  - The activations are bf16 and not rounded (the numerics of
  *    qlin_linear_weight_only): products of inputs and codes are exact, sums are
  *    f32 per group, scaled in f32 and added in f32.
@@ -117,9 +119,9 @@ typedef enum qlin_score {
  * does not depend on rounding.  An expert whose logit is -infinity or NaN is
  * masked out: score 0, its bias counts for nothing, and it comes after every
  * other expert of the runs that stay (in index order, so ids are always k
- * different experts); +infinity counts as the
- * largest finite value, and so do infinite biases (NaN as the smallest).  A token whose
- * experts are all masked out gets weights 0.
+ * different experts); +infinity counts as the largest finite value, a bias of
+ * +infinity or -infinity as the largest or smallest one, a bias of NaN as the
+ * smallest.  A token whose experts are all masked out gets weights 0.
  * 1 <= k <= min(QLIN_MAX_CHOICES, top_groups * E / groups), E <= QLIN_MAX_EXPERTS,
  * groups <= QLIN_MAX_GROUPS a divisor of E, 1 <= top_groups <= groups
  * (QLIN_ERR_SHAPE).  logits aligned to their type, ids and weights to 4 bytes.
@@ -140,8 +142,10 @@ int64_t qlin_experts_w4_workspace(int64_t T, int32_t k, int64_t E, int64_t H, in
  * token without experts gets zeros.  An expert may be chosen twice.  h is the
  * only value rounded on the way (it is a matrix-core operand): to bf16 where
  * many rows share an expert's weights and the matrix cores bound the call, to
- * two bf16 parts (16 bits) where they do not.  The sums, including the one over
- * the experts, are f32 in the order of j.
+ * two bf16 parts (16 bits) where they do not.  The sums are f32 in a fixed order:
+ * that over the experts in the order of j, but for few tokens, whose slots are
+ * multiplied one by one: there consecutive shares of the (j, input) pairs are
+ * summed with the weights applied, and then added in order.
  *   x bf16 [T, H]; ids [T, k], weights f32 [T, k] (qlin_route writes both);
  *   gate, up: E matrices [I, H]; down: E matrices [H, I]; one group size for
  *   all three (H and I multiples of it); y bf16 [T, H].

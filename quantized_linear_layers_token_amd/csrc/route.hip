@@ -15,8 +15,8 @@
 // order) and a ballot of its holders; only where several experts share the key
 // are their f64 choices compared.  Bound by vector instructions from some
 // thousand tokens on, below by the launch: 4096 tokens, 256 experts, sigmoid
-// and bias, the best 4 of 8 groups, 8 of 256: 10.1 us (12.6 with f64 keys
-// throughout); one token 2.7 us, an empty kernel 2.8.
+// and bias, the best 4 of 8 groups, 8 of 256: 9.6 us (12.6 with f64 keys
+// throughout); one token 2.6 us, an empty kernel 2.8.
 #include <cfloat>
 
 #include "qlin_device.h"

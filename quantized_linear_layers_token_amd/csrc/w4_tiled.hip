@@ -1,19 +1,25 @@
-// Products of many rows on 4-bit weights, tiled for the matrix cores:
-// BM = 16 MT rows of x by 256 weight rows per workgroup of four wavefronts.
+// Products of many rows on 4-bit weights, tiled for the matrix cores, in two
+// forms of 64 rows of x (BM) by 64 RT weight rows per workgroup:
+//   64 x 16 row tiles (RT = 4, KG = 1): four wavefronts, 256 weight rows;
+//   64 x 8 row tiles (RT = 2, KG = 2): two groups of four wavefronts, 128 weight
+//     rows; each group takes half of the input blocks with copies of x of its
+//     own, and the groups' sums are added through those copies at the end.  Half
+//     of the reuse of x and of the widened codes, for twice the workgroups: it is
+//     for sizes whose 64 x 16 tiles leave CUs idle.
 //
 // Bound by the matrix cores, next by the vector instructions that widen the
 // codes (seven per eight codes) and scale the group sums (four per 16 x 16
 // tile and group): both are shared by more tiles the larger a wavefront's part
-// is.  A wavefront takes 64 weight rows and all rows of x: its codes come
+// is.  A wavefront takes 16 RT weight rows and all rows of x: its codes come
 // straight from the packed order into registers, are widened once per
 // 128-input block and used for every row of x; the rows of x pass through LDS,
 // copied there in operand order without passing through registers, so that a
 // read is 16 contiguous bytes per lane.  The sums of x that the zero points
-// need are products with a constant operand, MT / 4 per wavefront and slice,
-// shared through LDS.  2048 x 4096 x 14336: 241 us, 1.0 PFLOP/s, the matrix
-// cores busy for half of the cycles at the 1.8 GHz that their power allows (the
-// library's bf16 product of that shape: 224 us); 64 experts of 2048 x 1024 with
-// 16384 rows: 187 us for gate and up, 117 for down.
+// need are products with a constant operand, one token tile per wavefront,
+// shared through LDS.  64 x 16, 2048 x 4096 x 14336: 233 - 246 us, 1.0 PFLOP/s, the
+// matrix cores busy for half of the cycles at the 1.8 GHz that their power allows
+// (the library's bf16 product of that shape: 224 us); 64 experts of 2048 x 1024 with
+// 16384 rows: 166 - 187 us for gate and up, 109 - 117 for down.
 #include "w4_device.h"
 
 namespace qlin {
@@ -282,6 +288,8 @@ __global__ __launch_bounds__(256 * KG, 2) void w4_tiled_kernel(W4Call c, int KT,
             }
         }
     };
+    // The experts' h is rounded to one bf16 here (2^-8 of it; y's error against 64
+    // bits 1.7e-3 -> 2.3e-3): a second part would double the matrix products of down.
     if constexpr (PAIR)
         store([&](int64_t at, int r, int mt, int i) {
             ((__attribute__((address_space(1))) uint16_t*)y)[at] =
