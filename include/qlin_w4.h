@@ -98,7 +98,7 @@ qlin_status qlin_linear_swiglu_w4(const uint16_t* x, int64_t M, int64_t K, int32
 
 typedef enum qlin_score {
     QLIN_SCORE_SOFTMAX = 0,  /* over the token's E logits */
-    QLIN_SCORE_SIGMOID = 1   /* of each logit */
+    QLIN_SCORE_SIGMOID = 1   /* of each logit; 0 below a logit of -708, where f64 ends */
 } qlin_score;
 
 /* Chooses k of E experts for each of T tokens.
