@@ -189,7 +189,7 @@ def prepare(case, seed):
         import quantized_linear_layers_token_amd as Q
         s["kv"] = Q.KVCache(*(s["cache"][n] for n in ("k", "v", "k_scale", "v_scale")))
         if op == "attn":
-            s["workspace"] = torch.empty(Q.qlin_attn_decode_workspace(case["S"], case["heads"], s["kv"]), dtype=torch.uint8, device="cuda")
+            s["workspace"] = torch.empty(Q.qlin_attn_decode_workspace(case["heads"], s["kv"]), dtype=torch.uint8, device="cuda")
     return s
 
 
