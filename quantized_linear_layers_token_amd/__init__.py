@@ -26,7 +26,7 @@ PATH_LARGE_256X128, PATH_LARGE_128X128, PATH_LARGE_128X64, PATH_LARGE_128X256 = 
 PATH_LARGE_128X128_K2, PATH_LARGE_128X64_K2 = 8, 9
 PATH_LARGE_256X256_W8 = 10   # int8 and FP8 rowwise only
 PATH_LARGE_256X256 = 11      # int8 and FP8 rowwise only
-ABI_VERSION = 4
+ABI_VERSION = 5
 NOALLOC_MAX_CODE_BYTES = 16 << 20    # staging capacity of qlin_linear_noalloc
 NOALLOC_MAX_SCALES = 1 << 20
 MAX_K = 131072
@@ -73,6 +73,38 @@ SIGNATURES_W4 = {
     "qlin_experts_w4": (_S, [_P, _I64, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
+# include/qlin_layer.h: norm, rotary positions, cache, attention of one token
+CACHE_BF16, CACHE_INT8, CACHE_FP8 = 0, 1, 2
+MAX_HEADS, MAX_HEAD_DIM = 1024, 256
+SIGNATURES_LAYER = {
+    "qlin_norm_bf16": (_S, [_P, _P, _P, _I64, _I64, _F, _P, _P, _P]),
+    "qlin_norm_int8": (_S, [_P, _P, _P, _I64, _I64, _F, _P, _P, _P, _P]),
+    "qlin_norm_fp8": (_S, [_P, _P, _P, _I64, _I64, _F, _I32, _P, _P, _P, _P]),
+    "qlin_rope": (_S, [_P, _I64, _P, _I64, _I32, _I32, _P, _P, _F, _P, _I64, _P]),
+    "qlin_cache_write": (_S, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F, _P, _P]),
+    "qlin_cache_read": (_S, [_P, _P, _I64, _P, _P, _P]),
+    "qlin_attn_decode_workspace": (_I64, [_I32, _I32, _I32]),
+    "qlin_attn_decode": (_S, [_P, _P, _P, _I64, _I32, _I64, _P, _I64, _F, _P, _P, _P]),
+}
+
+
+class QlinRotation(ctypes.Structure):
+    """struct qlin_rotation."""
+    _fields_ = [("frequencies", ctypes.c_void_p), ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("strength", ctypes.c_float)]
+
+
+class QlinKVCache(ctypes.Structure):
+    """struct qlin_kv_cache: the keys and values of one layer."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("kind", ctypes.c_int32)]
+
+
+class QlinQueries(ctypes.Structure):
+    """struct qlin_queries: the queries of a qlin_cache_write."""
+    _fields_ = [("q", ctypes.c_void_p), ("stride", ctypes.c_int64), ("gamma", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
 
 class QlinW4Weight(ctypes.Structure):
     """struct qlin_w4_weight: one packed 4-bit matrix, or one per expert."""
@@ -104,7 +136,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     if lib.qlin_abi_version() != ABI_VERSION:      # (int and no arguments: ctypes' default) before a symbol can be missing
         raise ImportError(f"libqlin ABI {lib.qlin_abi_version()} != binding ABI {ABI_VERSION}")
-    for name, (res, args) in {**SIGNATURES, **SIGNATURES_W4}.items():
+    for name, (res, args) in {**SIGNATURES, **SIGNATURES_W4, **SIGNATURES_LAYER}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
@@ -545,3 +577,278 @@ def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
         raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
     _launch(_lib.qlin_experts_w4, device, stream, x.data_ptr(), T, H, I, E, k, group, ids.data_ptr(), weights.data_ptr(),
             gate._bytes, up._bytes, down._bytes, y.data_ptr(), workspace.data_ptr())
+
+
+# --------------------------------------------------------------------------
+# Between the projections of a layer (include/qlin_layer.h).  As the calls
+# above, these run on the device of their first tensor.
+# --------------------------------------------------------------------------
+
+import math as _math  # noqa: E402
+
+
+def _norm_args(x, gamma, residual, sum_out):
+    """-> (device, M, K) after the checks that the norms share."""
+    device, M, K = _w4_input(x)
+    _w4_tensor(gamma, "gamma", (K,), 2, device)
+    if (residual is None) != (sum_out is None):
+        raise ValueError("residual and sum_out come together")
+    if residual is not None:
+        _w4_tensor(residual, "residual", (M, K), 2, device)
+        _w4_tensor(sum_out, "sum_out", (M, K), 2, device)
+    return device, M, K
+
+
+def qlin_norm_bf16(x, gamma, y, residual=None, sum_out=None, eps=1e-6, stream=None):
+    """x bf16 [M, K]; gamma bf16 [K]; y bf16 [M, K] receives the RMS norm of x, or of x + residual, which goes to
+    sum_out (both bf16 [M, K]; sum_out may be residual itself)."""
+    device, M, K = _norm_args(x, gamma, residual, sum_out)
+    _w4_tensor(y, "y", (M, K), 2, device)
+    _launch(_lib.qlin_norm_bf16, device, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, K, eps, _ptr(sum_out), y.data_ptr())
+
+
+def qlin_norm_int8(x, gamma, q, s, residual=None, sum_out=None, eps=1e-6, stream=None):
+    """qlin_norm_bf16 rounded as qlin_quant_act_int8 does, in one launch: q int8 [M, K], s f32 [M]."""
+    device, M, K = _norm_args(x, gamma, residual, sum_out)
+    _w4_tensor(q, "q", (M, K), 1, device)
+    _w4_tensor(s, "s", (M,), 4, device)
+    _launch(_lib.qlin_norm_int8, device, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, K, eps, _ptr(sum_out), q.data_ptr(),
+            s.data_ptr())
+
+
+def qlin_norm_fp8(x, gamma, q, s, group=0, residual=None, sum_out=None, eps=1e-6, stream=None):
+    """qlin_norm_bf16 rounded as qlin_quant_act_fp8 does: q E4M3 codes [M, K], s f32 [M] (group 0) or [M, K/128] (group 128)."""
+    device, M, K = _norm_args(x, gamma, residual, sum_out)
+    _w4_tensor(q, "q", (M, K), 1, device)
+    _w4_tensor(s, "s", (M, K // 128) if group == 128 else (M,), 4, device)
+    _launch(_lib.qlin_norm_fp8, device, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, K, eps, group, _ptr(sum_out), q.data_ptr(),
+            s.data_ptr())
+
+
+class _Fixed:
+    """A description that holds device addresses: its tensors cannot be replaced (their contents can be written), and
+    copies and pickles are built again from tensors of their own."""
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of a {type(self).__name__} cannot be replaced: build it anew")
+
+
+class Rope(_Fixed):
+    """Rotary positions of the first `dims` channels of a head: pair i turns by position * frequencies[i].
+
+    frequencies: f64 [dims / 2], or None for base ** (-2 i / dims) with `scaling`
+      "none";
+      "linear": divided by factor;
+      "ntk": of the base base * factor ** (dims / (dims - 2));
+      "yarn": pairs that make `fast` (32) or more turns within the `original` length as they are, those that make
+        `slow` (1) or fewer divided by factor, a ramp over the pairs between; strength 0.1 ln(factor) + 1;
+      "bands": as they are from `fast` (4) turns on, divided by factor up to `slow` (1), between by the turns.
+    interleaved: pairs are channels 2 i and 2 i + 1, else i and i + dims / 2.
+    strength: factor of cosine and sine (1, or as above)."""
+
+    def __init__(self, dims, base=10000.0, scaling="none", factor=1.0, original=None, interleaved=False, fast=None, slow=1.0,
+                 strength=None, frequencies=None, device="cuda"):
+        if dims < 16 or dims % 16 or dims > MAX_HEAD_DIM:
+            raise ValueError(f"dims must be a multiple of 16 from 16 to {MAX_HEAD_DIM}, not {dims}")
+        if frequencies is None:
+            values, default = self._values(dims, base, scaling, factor, original, fast, slow)
+            frequencies = _torch.tensor(values, dtype=_torch.float64, device=device)
+        else:
+            default = 1.0
+        if frequencies.dtype is not _torch.float64 or frequencies.shape != (dims // 2,) or not frequencies.is_contiguous():
+            raise ValueError(f"frequencies must be a contiguous float64 tensor of {dims // 2}")
+        strength = default if strength is None else float(strength)
+        vars(self).update(frequencies=frequencies, dims=dims, interleaved=bool(interleaved), strength=strength, device=frequencies.device,
+                          _bytes=bytes(QlinRotation(frequencies.data_ptr(), dims, 1 if interleaved else 0, strength)))
+
+    @staticmethod
+    def _values(dims, base, scaling, factor, original, fast, slow):
+        if not (base > 1 and factor > 0 and _math.isfinite(base) and _math.isfinite(factor)):
+            raise ValueError("base must be over 1 and factor over 0")
+        if scaling == "ntk":
+            base, factor, scaling = base * factor ** (dims / (dims - 2)), 1.0, "none"
+        plain = [base ** (-2.0 * i / dims) for i in range(dims // 2)]
+        if scaling == "none":
+            return plain, 1.0
+        if scaling == "linear":
+            return [f / factor for f in plain], 1.0
+        if scaling not in ("yarn", "bands"):
+            raise ValueError(f"scaling must be none, linear, ntk, yarn or bands, not {scaling!r}")
+        fast = (32.0 if scaling == "yarn" else 4.0) if fast is None else fast
+        if original is None or not original > 0 or not fast > slow > 0:
+            raise ValueError(f"{scaling} needs the original length, and fast over slow over 0")
+        if scaling == "bands":
+            stay = [(original * f / (2 * _math.pi) - slow) / (fast - slow) for f in plain]
+            default = 1.0
+        else:
+            def pair(turns):   # the (fractional) pair that makes so many turns
+                return dims * _math.log(original / (turns * 2 * _math.pi)) / (2 * _math.log(base))
+            first = max(_math.floor(pair(fast)), 0)
+            last = min(_math.ceil(pair(slow)), dims - 1)
+            stay = [1 - (i - first) / max(last - first, 0.001) for i in range(dims // 2)]
+            default = 0.1 * _math.log(factor) + 1 if factor > 1 else 1.0
+        stay = [min(max(w, 0.0), 1.0) for w in stay]
+        return [f * w + f / factor * (1 - w) for f, w in zip(plain, stay)], default
+
+    def __reduce__(self):
+        return _rope_again, (self.dims, self.interleaved, self.strength, self.frequencies)
+
+
+def _rope_again(dims, interleaved, strength, frequencies):
+    return Rope(dims, interleaved=interleaved, strength=strength, frequencies=frequencies)
+
+
+_KINDS = {_torch.bfloat16: CACHE_BF16, _torch.int8: CACHE_INT8, _torch.uint8: CACHE_FP8, _torch.float8_e4m3fn: CACHE_FP8}
+
+
+class KVCache(_Fixed):
+    """The paged keys and values of one layer: k and v [pages, kv_heads, page_size, dim], bfloat16, int8 or E4M3
+    (float8_e4m3fn or uint8 codes), the last two with k_scale and v_scale f32 [pages, kv_heads, page_size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.dtype not in _KINDS or v.dtype != k.dtype:
+            raise ValueError("k and v must be [pages, kv_heads, page_size, dim] tensors of bfloat16, int8, float8_e4m3fn or uint8")
+        kind, device, shape = _KINDS[k.dtype], k.device, tuple(k.shape)
+        for name, t in (("k", k), ("v", v)):
+            _w4_tensor(t, name, shape, 2 if kind == CACHE_BF16 else 1, device)
+        if kind == CACHE_BF16:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+        else:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or t.dtype is not _torch.float32:
+                    raise ValueError(f"{name} must be float32 [pages, kv_heads, page_size]")
+                _w4_tensor(t, name, shape[:3], 4, device)
+        pages, kv_heads, page_size, dim = shape
+        if max(pages, kv_heads, page_size, dim) > 0x7fffffff:
+            raise QlinError(QLIN_ERR_SHAPE, "KVCache")
+        vars(self).update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, pages=pages, kv_heads=kv_heads, page_size=page_size, dim=dim, kind=kind,
+                          device=device, _workspaces={}, _bytes=bytes(QlinKVCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages, kv_heads,
+                                                                  page_size, dim, kind)))
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_size, dim, dtype=_torch.float8_e4m3fn, device="cuda"):
+        """A cache of zeros."""
+        if dtype not in _KINDS:
+            raise ValueError("dtype must be bfloat16, int8, float8_e4m3fn or uint8")
+        shape = (pages, kv_heads, page_size, dim)
+        k, v = (_torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        scales = () if _KINDS[dtype] == CACHE_BF16 else tuple(_torch.zeros(shape[:3], dtype=_torch.float32, device=device) for _ in range(2))
+        return cls(k, v, *scales)
+
+    def __reduce__(self):
+        return KVCache, (self.k, self.v, self.k_scale, self.v_scale)
+
+
+def _heads(t, name, heads, dim, device, T=None):
+    """-> stride between the tokens of t, bf16 [T, heads, dim] with contiguous heads and any stride between tokens."""
+    if t.dtype not in _TYPES[2] or t.dim() != 3 or t.device != device:
+        if t.dtype is _torch.float16:
+            raise ValueError(f"{name} must be bfloat16 (or its bit patterns), not float16")
+        raise ValueError(f"{name} must be a 3-D tensor of 2-byte elements on {device}")
+    n, h, d = t.shape
+    if h != heads or d != dim or (T is not None and n != T):
+        raise ValueError(f"{name} must be [{'T' if T is None else T}, {heads}, {dim}], not {list(t.shape)}")
+    between, inner, last = t.stride()
+    if (last != 1 and d > 1) or (inner != d and h > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return between if n > 1 else h * d
+
+
+def _int32(t, name, shape, device):
+    if t.dtype is not _torch.int32:
+        raise ValueError(f"{name} must be int32 {list(shape)}")
+    _w4_tensor(t, name, shape, 4, device)
+
+
+def qlin_rope(x, positions, rope, y, gamma=None, eps=1e-6, stream=None):
+    """x bf16 [T, heads, dim] (any stride between tokens); positions int32 [T]; y like x, may be x, receives the rotated
+    heads.  gamma bf16 [dim]: each head's RMS norm first."""
+    device = x.device
+    if x.dim() != 3:
+        raise ValueError("x must be [T, heads, dim]")
+    T, heads, dim = x.shape
+    xs, ys = _heads(x, "x", heads, dim, device), _heads(y, "y", heads, dim, device, T)
+    _int32(positions, "positions", (T,), device)
+    if gamma is not None:
+        _w4_tensor(gamma, "gamma", (dim,), 2, device)
+    if rope.device != device:
+        raise ValueError(f"rope is on {rope.device}, the call runs on {device}")
+    _launch(_lib.qlin_rope, device, stream, x.data_ptr(), xs, positions.data_ptr(), T, heads, dim, rope._bytes, _ptr(gamma), eps, y.data_ptr(),
+            ys)
+
+
+_PACK_QUERIES = struct.Struct("QqQQqi4x").pack
+
+
+def qlin_cache_write(cache, slots, k, v, positions=None, rope=None, q=None, q_out=None, q_gamma=None, k_gamma=None, eps=1e-6, stream=None):
+    """k, v bf16 [T, kv_heads, dim] (any stride between tokens) into slots int32 [T] of the cache (-1: not written), and
+    q [T, heads, dim] into q_out (may be q), in one launch.  rope and positions int32 [T]: q and k are rotated;
+    q_gamma, k_gamma bf16 [dim]: each head's RMS norm first."""
+    device, dim = cache.device, cache.dim
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    _int32(slots, "slots", (T,), device)
+    ks, vs = _heads(k, "k", cache.kv_heads, dim, device, T), _heads(v, "v", cache.kv_heads, dim, device, T)
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions come together")
+    if rope is not None:
+        _int32(positions, "positions", (T,), device)
+        if rope.device != device:
+            raise ValueError(f"rope is on {rope.device}, the call runs on {device}")
+    if k_gamma is not None:
+        _w4_tensor(k_gamma, "k_gamma", (dim,), 2, device)
+    queries = None
+    if q is not None:
+        if q.dim() != 3 or q_out is None or (rope is None and q_gamma is None):
+            raise ValueError("q must be [T, heads, dim], with q_out, and rope or q_gamma")
+        heads = q.shape[1]
+        qs, os = _heads(q, "q", heads, dim, device, T), _heads(q_out, "q_out", heads, dim, device, T)
+        if q_gamma is not None:
+            _w4_tensor(q_gamma, "q_gamma", (dim,), 2, device)
+        queries = _PACK_QUERIES(q.data_ptr(), qs, _ptr(q_gamma) or 0, q_out.data_ptr(), os, heads)
+    elif q_out is not None or q_gamma is not None:
+        raise ValueError("q_out and q_gamma need q")
+    _launch(_lib.qlin_cache_write, device, stream, cache._bytes, slots.data_ptr(), T, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(positions),
+            None if rope is None else rope._bytes, _ptr(k_gamma), eps, queries)
+
+
+def qlin_cache_read(cache, slots, k, v, stream=None):
+    """k, v bf16 [n, kv_heads, dim] receive the keys and values of slots int32 [n]; rows of a slot outside the cache stay."""
+    device = cache.device
+    n = slots.shape[0] if slots.dim() == 1 else -1
+    _int32(slots, "slots", (n,), device)
+    shape = (n, cache.kv_heads, cache.dim)
+    _w4_tensor(k, "k", shape, 2, device)
+    _w4_tensor(v, "v", shape, 2, device)
+    _launch(_lib.qlin_cache_read, device, stream, cache._bytes, slots.data_ptr(), n, k.data_ptr(), v.data_ptr())
+
+
+def qlin_attn_decode_workspace(heads, cache):
+    """Bytes of qlin_attn_decode's workspace, for any number of sequences and any lengths."""
+    size = _lib.qlin_attn_decode_workspace(heads, cache.kv_heads, cache.dim)
+    if not size:
+        raise QlinError(QLIN_ERR_SHAPE, "qlin_attn_decode_workspace")
+    return size
+
+
+def qlin_attn_decode(q, cache, pages, lengths, out, workspace, scale=None, window=0, stream=None):
+    """Attention of one new token per sequence: q, out bf16 [S, heads, dim]; pages int32 [S, columns], the pages of each
+    sequence's tokens; lengths int32 [S] (0: out is zero, negative: left as it was); window > 0: the last tokens alone;
+    scale: dim ** -0.5 unless given; workspace uint8, qlin_attn_decode_workspace bytes."""
+    device, dim = cache.device, cache.dim
+    if q.dim() != 3 or pages.dim() != 2:
+        raise ValueError("q must be [S, heads, dim] and pages [S, columns]")
+    S, heads = q.shape[0], q.shape[1]
+    _w4_tensor(q, "q", (S, heads, dim), 2, device)
+    _w4_tensor(out, "out", (S, heads, dim), 2, device)
+    columns = pages.shape[1]
+    _int32(pages, "pages", (S, columns), device)
+    _int32(lengths, "lengths", (S,), device)
+    _w4_tensor(workspace, "workspace", None, 1, device)
+    need = cache._workspaces.get(heads)
+    if need is None:
+        need = cache._workspaces[heads] = _lib.qlin_attn_decode_workspace(heads, cache.kv_heads, dim)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
+    _launch(_lib.qlin_attn_decode, device, stream, q.data_ptr(), cache._bytes, pages.data_ptr(), S, heads, columns, lengths.data_ptr(), window,
+            dim ** -0.5 if scale is None else scale, out.data_ptr(), workspace.data_ptr())

@@ -1,0 +1,558 @@
+// Attention of one new token per sequence over the paged cache, split over the
+// tokens and joined.
+//
+// The cache is read once and bounds the call; everything else is arranged
+// around a steady stream of its rows.  A step of a wavefront takes 32 tokens
+// of one kv head and all query heads that read it (up to 16):
+//   S^T = K q^T   on 16x16x32 bf16 matrix instructions, K's rows straight from
+//                 memory as the first operand (codes widened to bf16, exactly),
+//                 so that a lane gets the scores of one head and 8 tokens;
+//   p = 2^(s - m) with the running maximum m of the head, in f32;
+//   O^T += V^T p^T  with the lane's own 8 tokens as its share of the inner
+//                 index: p never leaves the lane, and V's transpose is a
+//                 permutation of bytes within the lane (8 tokens x 4, 8 or 16
+//                 channels), done while its codes are widened.
+// The scale of a key multiplies its scores, that of a value its p.  p is split
+// in two bf16 parts (the matrix cores have the time: about a tenth of theirs
+// is used), which leaves 2^-17 of it.
+//
+// Work is cut in units of 32 tokens.  The units of all sequences, one after
+// the other, are shared evenly among `workers` workgroups per group of heads,
+// whatever the lengths: a workgroup finds its sequences by a scan of the
+// lengths.  A sequence within one workgroup is finished there; of one that
+// several share each writes a partial sum, and a second launch joins them.  So
+// the launches do not depend on the lengths and can be captured.
+#include "attn_index.h"
+#include "layer_device.h"
+
+namespace qlin {
+
+namespace {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef unsigned v8u __attribute__((ext_vector_type(8)));
+
+constexpr int kWaves = kAttnWaves;
+constexpr int kThreads = kWaves * kWave;
+constexpr float kNone = -__builtin_inff();    // score of no token
+
+struct AttnArgs {
+    const uint16_t* q;
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    const int *pages, *lengths;
+    uint16_t* out;
+    float* sums;      // partial sums [group of heads][worker][2][rows][dim + 2]
+    int* joins;       // [group of heads][worker][3]: sequence (-1: none), its last worker, the part of the first
+    int64_t npages;
+    int S, heads, kv_heads, dim, columns, page_size, window;
+    int tiles, rows, workers;
+    float scale;      // times log2 e
+};
+
+// Page tables and lengths are read through the scalar cache: a vector load
+// between those of the tiles would wait for all that were issued before it.
+typedef const __attribute__((address_space(4))) int* Table;
+__device__ __forceinline__ Table table_of(const int* p) { return (Table)(uintptr_t)p; }
+
+__device__ __forceinline__ AttnSpan span_of(int length, const AttnArgs& a) {
+    return attn_span(length, a.columns, a.page_size, a.window);
+}
+
+__device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// Slots between the last matrix instruction and the first read of its result
+// (one more than the four passes of a 16x16x32 need on this machine).
+__device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Maximum and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float column_max(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float column_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+__device__ __forceinline__ uint32_t bits(v2bf v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ v8bf operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return __builtin_bit_cast(v8bf, v4u{a, b, c, d}); }
+
+// Codes as bf16, exactly: a pair of bytes of w (E4M3: by one instruction;
+// int8: by way of f32, whose upper halves are the bf16 values).
+template <int KIND, bool HI>
+__device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
+    if constexpr (KIND == QLIN_CACHE_FP8) {
+        return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+    } else {
+        const float a = (float)(int8_t)(HI ? w >> 16 : w), b = (float)(int8_t)(HI ? w >> 24 : w >> 8);
+        return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+    }
+}
+
+// 8 channels of a row as an operand of S^T.
+template <int KIND>
+__device__ __forceinline__ v8bf key_operand(uint32_t a, uint32_t b) {
+    return operand(widen_pair<KIND, false>(a), widen_pair<KIND, true>(a), widen_pair<KIND, false>(b), widen_pair<KIND, true>(b));
+}
+
+// Head length DP = 64, 128 or 256 in registers; heads of dim < DP channels
+// read some channels twice, against zeros of q and without a place in out.
+template <int KIND, int DP>
+struct Tiles {
+    static constexpr int kBytes = KIND == QLIN_CACHE_BF16 ? 2 : 1;
+    static constexpr int kKeyChunks = DP / 4 * kBytes / 16;    // 16-byte chunks of a row per lane
+    static constexpr int kValueDwords = DP / 16 * kBytes / 4;  // dwords of a row per lane
+    v4u key[2][kKeyChunks];
+    uint32_t value[8][kValueDwords];
+    v4f key_scale[2], value_scale[2];
+};
+
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&to)[N]) {
+    if constexpr (N == 1) {
+        to[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const v2u t = *reinterpret_cast<const v2u*>(p);
+        to[0] = t.x, to[1] = t.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const v4u t = reinterpret_cast<const v4u*>(p)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[4 * i + j] = t[j];
+        }
+    }
+}
+
+template <int KIND, int DP>
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
+    using T = Tiles<KIND, DP>;
+    constexpr int kTiles = DP / 16, kSteps = DP / 32;
+    constexpr int kPad = DP + 4;
+    __shared__ float joined[2][kAttnHeads * kPad];
+    __shared__ float stats[2][2][kAttnHeads];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int n = lane & 15, g = lane >> 4;
+    const int group = blockIdx.x % (a.kv_heads * a.tiles), worker = blockIdx.x / (a.kv_heads * a.tiles);
+    const int kv_head = group / a.tiles, tile = group % a.tiles;
+    const int shared_by = a.heads / a.kv_heads;
+    const int head0 = kv_head * shared_by + tile * kAttnHeads;
+    const int rows = min(a.rows, shared_by - tile * kAttnHeads);
+    int* join = a.joins + ((int64_t)group * a.workers + worker) * 3;
+
+    // sequences without tokens, a share of them each
+    for (int s = worker * kWaves + wave; s < a.S; s += a.workers * kWaves)
+        if (a.lengths[s] == 0 || a.columns == 0)
+            if (a.lengths[s] >= 0)
+                for (int i = lane; i < rows * a.dim / 2; i += kWave)
+                    reinterpret_cast<uint32_t*>(a.out + ((int64_t)s * a.heads + head0) * a.dim)[i] = 0;
+
+    // the worker's units, and the sequence of the first of them
+    int64_t total = 0;
+    for (int s = lane; s < a.S; s += kWave) total += span_of(a.lengths[s], a).units;
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) total += __shfl_xor(total, m);
+    const int64_t share = attn_share(total, a.workers);
+    const int64_t lo = worker * share, hi = min(lo + share, total);
+    if (threadIdx.x == 0) join[0] = -1;
+    if (lo >= total) return;
+    int s = 0;
+    int64_t before = 0;   // units of the sequences before s
+    for (int c = 0; c < a.S; c += kWave) {
+        const unsigned u = c + lane < a.S ? span_of(a.lengths[c + lane], a).units : 0;
+        unsigned upto = u;
+#pragma unroll
+        for (int m = 1; m < kWave; m *= 2) {
+            const unsigned o = __shfl_up(upto, m);
+            upto += lane >= m ? o : 0;
+        }
+        const uint64_t past = __ballot(before + upto > lo);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            s = c + at;
+            before += (unsigned)__builtin_amdgcn_readlane((int)(upto - u), at);
+            break;
+        }
+        before += (unsigned)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+    }
+
+    const int64_t row_bytes = (int64_t)a.dim * T::kBytes;
+    // byte offsets in a row: the lane's quarter of the channels as 16-byte chunks (keys), its DP / 16 channels (values)
+    int key_at[T::kKeyChunks];
+#pragma unroll
+    for (int i = 0; i < T::kKeyChunks; ++i) {
+        const int at = g * (DP / 4 * T::kBytes) + 16 * i;
+        key_at[i] = n * (int)row_bytes + (at < row_bytes ? at : 0);
+    }
+    const int value_piece = n * (DP / 16 * T::kBytes);
+    const int value_at = 4 * g * (int)row_bytes + (value_piece < row_bytes ? value_piece : 0);
+
+    for (; s < a.S && before < hi; ++s) {
+        s = __builtin_amdgcn_readfirstlane(s);
+        const AttnSpan span = span_of(table_of(a.lengths)[s], a);
+        if (span.units == 0) continue;
+        const int first = (int)(max(lo, before) - before), last = (int)(min(hi, before + span.units) - before);
+        // the wavefront's units of them
+        const int mine = first + (int)((int64_t)(last - first) * wave / kWaves);
+        const int end = first + (int)((int64_t)(last - first) * (wave + 1) / kWaves);
+
+        v8bf q[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int d = g * (DP / 4) + 8 * i;
+            v4u w = v4u{0, 0, 0, 0};
+            if (n < rows && d < a.dim) w = *reinterpret_cast<const v4u*>(a.q + ((int64_t)s * a.heads + head0 + n) * a.dim + d);
+            q[i] = __builtin_bit_cast(v8bf, w);
+        }
+
+        const Table table = table_of(a.pages + (int64_t)s * a.columns);
+        struct Places {
+            AttnPlace at[2];
+        };
+        auto where = [&](int unit) {
+            Places p;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                p.at[j] = attn_place(span, unit, j, table, (int)a.npages, a.kv_heads, kv_head, a.page_size);
+            return p;
+        };
+        auto load_keys = [&](const Places& p, T& t) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* base = a.k + p.at[j].row * row_bytes;
+#pragma unroll
+                for (int i = 0; i < T::kKeyChunks; ++i) t.key[j][i] = *reinterpret_cast<const v4u*>(base + key_at[i]);
+                if constexpr (KIND != QLIN_CACHE_BF16) t.key_scale[j] = reinterpret_cast<const v4f*>(a.k_scale + p.at[j].row)[g];
+            }
+        };
+        auto load_values = [&](const Places& p, T& t) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* base = a.v + p.at[j].row * row_bytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) load_dwords(base + value_at + i * row_bytes, t.value[4 * j + i]);
+                if constexpr (KIND != QLIN_CACHE_BF16) t.value_scale[j] = reinterpret_cast<const v4f*>(a.v_scale + p.at[j].row)[g];
+            }
+        };
+
+        float m = kNone, l = 0.0f;
+        v4f acc[kTiles];
+#pragma unroll
+        for (int r = 0; r < kTiles; ++r) acc[r] = v4f{0, 0, 0, 0};
+
+        T t;
+        Places here, next;
+        if (mine < end) {
+            here = where(mine);
+            load_keys(here, t);
+            load_values(here, t);
+        }
+        for (int unit = mine; unit < end; ++unit) {
+            const bool more = unit + 1 < end;
+            if (more) next = where(unit + 1);
+            v4f score[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    v8bf k;
+                    if constexpr (KIND == QLIN_CACHE_BF16) k = __builtin_bit_cast(v8bf, t.key[j][i]);
+                    else k = key_operand<KIND>(t.key[j][i / 2][2 * (i % 2)], t.key[j][i / 2][2 * (i % 2) + 1]);
+                    score[j] = mfma(k, q[i], score[j]);
+                }
+            }
+            v4f key_scale[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) key_scale[j] = KIND == QLIN_CACHE_BF16 ? v4f{1, 1, 1, 1} : t.key_scale[j];
+            if (more) load_keys(next, t);
+            settle();
+            float p[8], top = kNone;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 4 * g + i;
+                    const float x = score[j][i] * (KIND == QLIN_CACHE_BF16 ? a.scale : key_scale[j][i] * a.scale);
+                    p[4 * j + i] = at >= here.at[j].lo && at < here.at[j].hi ? x : kNone;
+                    top = fmaxf(top, p[4 * j + i]);
+                }
+            }
+            top = column_max(top);
+            if (__any(top > m)) {
+                const float now = fmaxf(m, top);
+                const float by = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+                m = now;
+                l *= by;
+#pragma unroll
+                for (int r = 0; r < kTiles; ++r) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][i] *= by;
+                }
+            }
+            const float zero_at = m == kNone ? 0.0f : m;
+            const bool whole = here.at[0].lo == 0 && here.at[1].lo == 0 && here.at[0].hi == 16 && here.at[1].hi == 16;
+            if (!whole) {   // what lies in masked places may be anything
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = 4 * g + i;
+                        const bool live = at >= here.at[j].lo && at < here.at[j].hi;
+#pragma unroll
+                        for (int w = 0; w < T::kValueDwords; ++w) t.value[4 * j + i][w] = live ? t.value[4 * j + i][w] : 0;
+                        if constexpr (KIND != QLIN_CACHE_BF16) t.value_scale[j][i] = live ? t.value_scale[j][i] : 0.0f;
+                    }
+                }
+            }
+            v8bf high, low;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(p[4 * j + i] - zero_at);
+                    l += e;
+                    const float x = KIND == QLIN_CACHE_BF16 ? e : e * t.value_scale[j][i];
+                    high[4 * j + i] = (__bf16)x;
+                    low[4 * j + i] = (__bf16)(x - (float)high[4 * j + i]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < T::kValueDwords; ++w) {
+                // dword w of the 8 tokens: channels (of the lane) 4 w .. 4 w + 3, or 2 w, 2 w + 1 in bf16
+                if constexpr (KIND == QLIN_CACHE_BF16) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t pick = h ? 0x07060302u : 0x05040100u;
+                        uint32_t d[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_perm(t.value[2 * i + 1][w], t.value[2 * i][w], pick);
+                        const v8bf v = operand(d[0], d[1], d[2], d[3]);
+                        acc[2 * w + h] = mfma(v, high, acc[2 * w + h]);
+                        acc[2 * w + h] = mfma(v, low, acc[2 * w + h]);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // bytes 2 h and 2 h + 1 of two tokens: {a, b, a', b'}
+                        const uint32_t pick = h ? 0x07030602u : 0x05010400u;
+                        uint32_t x[4], y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t both = __builtin_amdgcn_perm(t.value[2 * i + 1][w], t.value[2 * i][w], pick);
+                            x[i] = widen_pair<KIND, false>(both);
+                            y[i] = widen_pair<KIND, true>(both);
+                        }
+                        const v8bf v0 = operand(x[0], x[1], x[2], x[3]), v1 = operand(y[0], y[1], y[2], y[3]);
+                        acc[4 * w + 2 * h] = mfma(v0, high, acc[4 * w + 2 * h]);
+                        acc[4 * w + 2 * h + 1] = mfma(v1, high, acc[4 * w + 2 * h + 1]);
+                        acc[4 * w + 2 * h] = mfma(v0, low, acc[4 * w + 2 * h]);
+                        acc[4 * w + 2 * h + 1] = mfma(v1, low, acc[4 * w + 2 * h + 1]);
+                    }
+                }
+            }
+            if (more) {
+                load_values(next, t);
+                here = next;
+            }
+        }
+        settle();
+        l = column_sum(l);
+
+        // The four wavefronts' sums, joined in pairs: 2 and 3 hand theirs to 0
+        // and 1, then 1 to 0.  acc[r][i] is channel (DP / 16) (4 g + i) + r of head n.
+        auto give = [&](int slot) {
+            if (n < rows) {
+                float* to = joined[slot] + n * kPad + 4 * g * kTiles;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int r = 0; r < kTiles; ++r) to[i * kTiles + r] = acc[r][i];
+                }
+                if (g == 0) stats[slot][0][n] = m, stats[slot][1][n] = l;
+            }
+        };
+        auto take = [&](int slot) {
+            if (n < rows) {
+                const float om = stats[slot][0][n], now = fmaxf(m, om), zero_at = now == kNone ? 0.0f : now;
+                const float by = __builtin_amdgcn_exp2f(m - zero_at), other = __builtin_amdgcn_exp2f(om - zero_at);
+                const float* from = joined[slot] + n * kPad + 4 * g * kTiles;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int r = 0; r < kTiles; ++r) acc[r][i] = acc[r][i] * by + from[i * kTiles + r] * other;
+                }
+                l = l * by + stats[slot][1][n] * other;
+                m = now;
+            }
+        };
+        __syncthreads();   // the buffers are free
+        if (wave >= 2) give(wave - 2);
+        __syncthreads();
+        if (wave < 2) take(wave);
+        __syncthreads();
+        if (wave == 1) give(0);
+        __syncthreads();
+        if (wave == 0) take(0);
+
+        const bool starts = before >= lo, ends = before + span.units <= hi;
+        if (wave == 0 && n < rows) {
+            const int d0 = 4 * g * kTiles;
+            if (starts && ends) {
+                const float by = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                uint16_t* to = a.out + ((int64_t)s * a.heads + head0 + n) * a.dim + d0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int r = 0; r < kTiles; r += 2)
+                        if (d0 + i * kTiles + r < a.dim)
+                            *reinterpret_cast<uint32_t*>(to + i * kTiles + r) = bf16_pair(acc[r][i] * by, acc[r + 1][i] * by);
+                }
+            } else {
+                const int part = attn_part(before, lo);
+                float* to = a.sums + ((((int64_t)group * a.workers + worker) * 2 + part) * a.rows + n) * (a.dim + 2);
+                if (g == 0) to[0] = m, to[1] = l;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int r = 0; r < kTiles; r += 2)
+                        if (d0 + i * kTiles + r < a.dim)
+                            *reinterpret_cast<v2f*>(to + 2 + d0 + i * kTiles + r) = v2f{acc[r][i], acc[r + 1][i]};
+                }
+                if (starts && lane == 0) {
+                    join[0] = s;
+                    join[1] = attn_last_worker(before, span.units, share);
+                    join[2] = part;
+                }
+            }
+        }
+        before += span.units;
+    }
+}
+
+// A workgroup joins the parts of the sequence that began with a worker and went
+// on, for one query head: the wavefronts take every fourth part.
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+    __shared__ float part_max[kWaves], part_sum[kWaves];
+    __shared__ float part_out[kWaves][QLIN_MAX_HEAD_DIM];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int worker = blockIdx.x % a.workers, at = blockIdx.x / a.workers;
+    const int group = at / a.rows, row = at % a.rows;
+    const int* join = a.joins + ((int64_t)group * a.workers + worker) * 3;
+    const int s = join[0];
+    const int shared_by = a.heads / a.kv_heads, tile = group % a.tiles;
+    if (s < 0 || tile * kAttnHeads + row >= shared_by) return;
+    const int last = join[1], part = join[2];
+    auto sums = [&](int w) {
+        return a.sums + ((((int64_t)group * a.workers + w) * 2 + (w == worker ? part : 0)) * a.rows + row) * (a.dim + 2);
+    };
+    // each wavefront keeps a running maximum of its own
+    float m = kNone, l = 0.0f, o[4] = {0, 0, 0, 0};
+    for (int w = worker + wave; w <= last; w += kWaves) {
+        const float* p = sums(w);
+        const float pm = p[0], pl = p[1];
+        v2f x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int d = 2 * lane + 128 * i;
+            x[i] = d < a.dim ? *reinterpret_cast<const v2f*>(p + 2 + d) : v2f{0, 0};
+        }
+        const float now = fmaxf(m, pm), zero_at = now == kNone ? 0.0f : now;
+        const float by = __builtin_amdgcn_exp2f(m - zero_at), other = __builtin_amdgcn_exp2f(pm - zero_at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = o[i] * by + x[i / 2][i % 2] * other;
+        l = l * by + pl * other;
+        m = now;
+    }
+    if (lane == 0) part_max[wave] = m, part_sum[wave] = l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part_out[wave][2 * lane + 128 * (i / 2) + i % 2] = o[i];
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= a.dim) return;
+    float top = kNone;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, part_max[w]);
+    top = top == kNone ? 0.0f : top;
+    float sum = 0.0f, out = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const float by = __builtin_amdgcn_exp2f(part_max[w] - top);
+        sum += part_sum[w] * by;
+        out += part_out[w][d] * by;
+    }
+    const int head = group / a.tiles * shared_by + tile * kAttnHeads + row;
+    a.out[((int64_t)s * a.heads + head) * a.dim + d] = f32_to_bf16(sum > 0.0f || sum != sum ? out / sum : 0.0f);
+}
+
+template <int KIND>
+void launch_kind(const AttnArgs& a, unsigned grid, hipStream_t st) {
+    if (a.dim <= 64) hipLaunchKernelGGL((attn_kernel<KIND, 64>), dim3(grid), dim3(kThreads), 0, st, a);
+    else if (a.dim <= 128) hipLaunchKernelGGL((attn_kernel<KIND, 128>), dim3(grid), dim3(kThreads), 0, st, a);
+    else hipLaunchKernelGGL((attn_kernel<KIND, 256>), dim3(grid), dim3(kThreads), 0, st, a);
+}
+
+constexpr int kResident = 512;   // workgroups of four wavefronts that the card holds at once: two on each CU
+
+}  // namespace
+
+AttnShape attn_shape(int heads, int kv_heads, int dim) {
+    (void)dim;
+    const int shared_by = heads / kv_heads, tiles = (shared_by + kAttnHeads - 1) / kAttnHeads;
+    const int groups = kv_heads * tiles;
+    return AttnShape{tiles, shared_by < kAttnHeads ? shared_by : kAttnHeads, groups >= kResident ? 1 : kResident / groups};
+}
+
+int64_t attn_workspace(int heads, int kv_heads, int dim) {
+    const AttnShape s = attn_shape(heads, kv_heads, dim);
+    const int64_t records = (int64_t)kv_heads * s.tiles * s.workers;
+    return records * 2 * s.rows * (dim + 2) * 4 + (records * 3 * 4 + 15) / 16 * 16;
+}
+
+hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
+    const AttnShape shape = attn_shape(c.heads, c.cache.kv_heads, c.cache.dim);
+    const int groups = c.cache.kv_heads * shape.tiles;
+    AttnArgs a{};
+    a.q = c.q;
+    a.k = static_cast<const uint8_t*>(c.cache.k);
+    a.v = static_cast<const uint8_t*>(c.cache.v);
+    a.k_scale = c.cache.k_scale;
+    a.v_scale = c.cache.v_scale;
+    a.pages = c.pages;
+    a.lengths = c.lengths;
+    a.out = c.out;
+    a.sums = static_cast<float*>(c.workspace);
+    a.joins = reinterpret_cast<int*>(a.sums + (int64_t)groups * shape.workers * 2 * shape.rows * (c.cache.dim + 2));
+    a.npages = c.cache.pages;
+    a.S = c.S;
+    a.heads = c.heads;
+    a.kv_heads = c.cache.kv_heads;
+    a.dim = c.cache.dim;
+    a.columns = c.columns;
+    a.page_size = c.cache.page_size;
+    a.window = c.window;
+    a.tiles = shape.tiles;
+    a.rows = shape.rows;
+    a.workers = shape.workers;
+    a.scale = c.scale * 1.44269504088896340736f;
+    const unsigned grid = (unsigned)(groups * shape.workers);
+    if (c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(a, grid, st);
+    else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(a, grid, st);
+    else launch_kind<QLIN_CACHE_FP8>(a, grid, st);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && shape.workers > 1) {
+        hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(groups * shape.rows * shape.workers)), dim3(kThreads), 0, st, a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace qlin

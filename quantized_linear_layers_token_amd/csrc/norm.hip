@@ -1,0 +1,175 @@
+// RMS norm of bf16 rows with the residual's addition, rounded for the next
+// projection (bf16, int8 or OCP E4M3 by the token or by 128 inputs).
+//
+// One pass over the row: it stays in registers as the bf16 it is rounded to
+// (r = bf16(x + residual)), and one reduction gives both statistics.  With
+// t = r * gamma (exact in f32) and d = 1 / sqrt(mean r^2 + eps) the normalised
+// value is t * d; its code for the absmax a * d is the code of t for the absmax
+// a, since d cancels out of t * d * (Q / (a * d)).  So the codes wait for
+// max |t| alone and only the scale, a * d / Q, takes the sum of squares.
+#include <type_traits>
+
+#include "layer_device.h"
+
+namespace qlin {
+
+namespace {
+
+__device__ __forceinline__ v4u add8(const v4u& a, const v4u& b) {
+    v4u r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = bf16_pair(bf16_lo(a[i]) + bf16_lo(b[i]), bf16_hi(a[i]) + bf16_hi(b[i]));
+    return r;
+}
+
+// THREADS lanes per row, ROWS rows per workgroup (more than one only for rows
+// of one wavefront); CPT 16-byte chunks of the row per thread.
+template <int THREADS, int ROWS, int CPT, int OUT>
+__global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
+    static_assert(ROWS == 1 || THREADS == kWave, "a row of several wavefronts takes the workgroup's barrier");
+    constexpr int kWaves = THREADS / kWave;
+    constexpr bool kKeepGamma = CPT <= 4;   // held for the second use where registers allow, else read again
+    constexpr int kBatch = CPT < 4 ? CPT : 4;   // chunks whose loads are under way together
+    __shared__ float red[2 * kWaves];
+    const int tid = ROWS > 1 ? threadIdx.x % THREADS : threadIdx.x;
+    const int64_t m = ROWS > 1 ? (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS : blockIdx.x;
+    if (ROWS > 1 && m >= a.M) return;
+    const int nchunks = (int)(a.K >> 3);
+    const v4u* x = reinterpret_cast<const v4u*>(a.x + m * a.K);
+    const v4u* res = a.residual ? reinterpret_cast<const v4u*>(a.residual + m * a.K) : nullptr;
+    const v4u* gamma = reinterpret_cast<const v4u*>(a.gamma);
+    const v4u zero = v4u{0, 0, 0, 0};
+
+    v4u r[CPT], g[kKeepGamma ? CPT : 1];
+    if constexpr (kKeepGamma) {
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            const int c = tid + j * THREADS;
+            g[j] = c < nchunks ? gamma[c] : zero;
+        }
+    }
+#pragma unroll
+    for (int j0 = 0; j0 < CPT; j0 += kBatch) {
+#pragma unroll
+        for (int j = j0; j < j0 + kBatch; ++j) {
+            const int c = tid + j * THREADS;
+            r[j] = c < nchunks ? x[c] : zero;
+        }
+        if (res) {
+            v4u* sum = reinterpret_cast<v4u*>(a.sum + m * a.K);
+            v4u b[kBatch];
+#pragma unroll
+            for (int j = j0; j < j0 + kBatch; ++j) {
+                const int c = tid + j * THREADS;
+                b[j - j0] = c < nchunks ? res[c] : zero;
+            }
+#pragma unroll
+            for (int j = j0; j < j0 + kBatch; ++j) {
+                const int c = tid + j * THREADS;
+                r[j] = add8(r[j], b[j - j0]);
+                if (c < nchunks) sum[c] = r[j];
+            }
+        }
+    }
+
+    float squares = 0.0f, amax = 0.0f, group[OUT == kNormFp8Block ? CPT : 1];
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+        const int c = tid + j * THREADS;
+        v4u gj;
+        if constexpr (kKeepGamma) gj = g[j];
+        else gj = c < nchunks ? gamma[c] : zero;
+        float f[8], w[8], top = 0.0f;
+        widen8(r[j], f);
+        widen8(gj, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares);
+        if constexpr (OUT != kNormBf16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i] * w[i]));
+        }
+        if constexpr (OUT == kNormFp8Block) group[j] = lanes_max<16>(top);   // 16 chunks: 128 inputs
+        else amax = fmaxf(amax, top);
+    }
+    squares = wave_sum_f32(squares);
+    if constexpr (OUT == kNormInt8 || OUT == kNormFp8) amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
+    if constexpr (kWaves > 1) {
+        const int wave = threadIdx.x / kWave;
+        if (threadIdx.x % kWave == 0) red[wave] = squares, red[kWaves + wave] = amax;
+        __syncthreads();
+        squares = red[0], amax = red[kWaves];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) squares += red[w], amax = fmaxf(amax, red[kWaves + w]);
+    }
+    const float d = 1.0f / sqrtf(squares / (float)a.K + a.eps);
+
+    constexpr bool kFp8 = OUT == kNormFp8 || OUT == kNormFp8Block;
+    Rounding rr = {};
+    if constexpr (OUT == kNormInt8 || OUT == kNormFp8) {
+        rr = rounding<kFp8>(amax);
+        if (tid == 0) a.s[m] = amax * d / (kFp8 ? 448.0f : 127.0f);
+    }
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+        const int c = tid + j * THREADS;
+        if (c >= nchunks) break;
+        v4u gj;
+        if constexpr (kKeepGamma) gj = g[j];
+        else gj = gamma[c];
+        float f[8], w[8];
+        widen8(r[j], f);
+        widen8(gj, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= w[i];
+        if constexpr (OUT == kNormBf16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= d;
+            reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.y) + m * a.K)[c] = narrow8(f);
+        } else {
+            if constexpr (OUT == kNormFp8Block) {
+                rr = rounding<true>(group[j]);
+                if (c % 16 == 0) a.s[m * (a.K / 128) + c / 16] = group[j] * d / 448.0f;
+            }
+            reinterpret_cast<v2u*>(static_cast<uint8_t*>(a.y) + m * a.K)[c] = codes8<kFp8>(f, rr);
+        }
+    }
+}
+
+template <int OUT>
+hipError_t launch_out(const NormCall& c, hipStream_t st) {
+    const int64_t chunks = c.K / 8;
+    auto go = [&](auto threads, auto rows, auto cpt) {
+        constexpr int T = decltype(threads)::value, R = decltype(rows)::value, C = decltype(cpt)::value;
+        hipLaunchKernelGGL((norm_kernel<T, R, C, OUT>), dim3((unsigned)((c.M + R - 1) / R)), dim3(T * R), 0, st, c);
+    };
+    using std::integral_constant;
+    integral_constant<int, 1> one;
+    integral_constant<int, 2> two;
+    integral_constant<int, 4> four;
+    integral_constant<int, 8> eight;
+    integral_constant<int, 16> sixteen;
+    integral_constant<int, 64> t64;
+    integral_constant<int, 256> t256;
+    integral_constant<int, 1024> t1024;
+    if (chunks <= 64) go(t64, four, one);
+    else if (chunks <= 256) go(t256, one, one);
+    else if (chunks <= 512) go(t256, one, two);
+    else if (chunks <= 1024) go(t256, one, four);
+    else if (chunks <= 4096) go(t1024, one, four);
+    else if (chunks <= 8192) go(t1024, one, eight);
+    else go(t1024, one, sixteen);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(NormOut out, const NormCall& c, hipStream_t st) {
+    switch (out) {
+        case kNormBf16: return launch_out<kNormBf16>(c, st);
+        case kNormInt8: return launch_out<kNormInt8>(c, st);
+        case kNormFp8: return launch_out<kNormFp8>(c, st);
+        default: return launch_out<kNormFp8Block>(c, st);
+    }
+}
+
+}  // namespace qlin
