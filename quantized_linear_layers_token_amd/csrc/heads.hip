@@ -4,10 +4,11 @@
 //
 // A workgroup takes one token: the cosines and sines of its position are
 // formed once, by dims / 2 threads, and shared by all of its heads through LDS.
-// LANES lanes hold a head, eight channels (16 bytes) each, so that the sum of
-// squares and the absmax are reductions within 8, 16 or 32 lanes and the other
-// channel of a pair is in the lane's own registers (neighbours) or comes from
-// one other lane (halves).
+// LANES lanes hold a head, eight channels each, so that the sum of squares and
+// the absmax are reductions within 8, 16 or 32 lanes.  A lane's channels are
+// two runs of four: both channels of each of its pairs, so that nothing is
+// exchanged for the rotation, and its cosines and sines are the same for every
+// head of the token and stay in registers.
 #include <type_traits>
 
 #include "layer_device.h"
@@ -17,7 +18,7 @@ namespace qlin {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;   // heads of each thread whose loads are under way together
+constexpr int kAhead = 3;   // heads of each thread whose loads are under way together
 
 // Cosine and sine of position * frequency, times strength.  The product is
 // reduced in f64 by multiples of 2 pi in two parts (the first exact to 53
@@ -39,92 +40,84 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
     constexpr int kPer = kThreads / LANES;   // heads that the workgroup takes at once
     const int64_t t = blockIdx.x;
     const int c = threadIdx.x % LANES, first = threadIdx.x / LANES;
-    const int chunks = a.dim / 8;
-    const bool mine = c < chunks;
-    const int64_t slots = a.cache.pages * a.cache.page_size;
-    const int slot = a.kv_heads ? a.slots[t] : -1;
-    const bool kept = slot >= 0 && slot < slots;
-    // a token that is not kept has no keys and values to do
-    const int all = a.heads + (kept ? 2 * a.kv_heads : 0);
-    const int page = kept ? slot / a.cache.page_size : 0, place = kept ? slot % a.cache.page_size : 0;
-    const int half = a.rope.dims / 16;       // chunks of half of the rotated channels
+    const bool mine = c < a.dim / 8;
+    // the lane's channels: lo .. lo + 3 and hi .. hi + 3
+    const int pairs = ROTATE ? a.rope.dims / 2 : 0;
+    int lo = 8 * c, hi = 8 * c + 4;
+    bool turned = ROTATE && 8 * c < 2 * pairs;
+    if constexpr (ROTATE && !NEIGHBOURS) {
+        if (turned) lo = 4 * c, hi = 4 * c + pairs;
+    }
+    const int all = a.heads + 2 * a.kv_heads;
     const uint16_t *q = a.q + t * a.q_stride, *k = a.k + t * a.k_stride, *v = a.v + t * a.v_stride;
+    const v2u none = v2u{0, 0};
+    v2u gamma[2][2] = {{none, none}, {none, none}};   // of queries and keys
+    const bool normed = a.q_gamma || a.k_gamma;
+    if (normed && mine) {
+        if (a.q_gamma) gamma[0][0] = *reinterpret_cast<const v2u*>(a.q_gamma + lo), gamma[0][1] = *reinterpret_cast<const v2u*>(a.q_gamma + hi);
+        if (a.k_gamma) gamma[1][0] = *reinterpret_cast<const v2u*>(a.k_gamma + lo), gamma[1][1] = *reinterpret_cast<const v2u*>(a.k_gamma + hi);
+    }
+    const int slot = a.kv_heads ? a.slots[t] : -1;
+    int64_t row0 = -1;    // row of the cache of the token's first head
+    float2 w[4];
 
-    for (int base = 0; base == 0 || base < all; base += kAhead * kPer) {
-        v4u raw[kAhead];
+    for (int base = 0; base < all; base += kAhead * kPer) {
+        v2u raw[kAhead][2];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int h = base + u * kPer + first;
-            raw[u] = v4u{0, 0, 0, 0};
+            raw[u][0] = raw[u][1] = none;
             if (mine && h < all) {
                 const uint16_t* p = h < a.heads ? q + h * a.dim
                                   : h < a.heads + a.kv_heads ? k + (h - a.heads) * a.dim
                                                              : v + (h - a.heads - a.kv_heads) * a.dim;
-                raw[u] = *reinterpret_cast<const v4u*>(p + 8 * c);
+                raw[u][0] = *reinterpret_cast<const v2u*>(p + lo);
+                raw[u][1] = *reinterpret_cast<const v2u*>(p + hi);
             }
         }
-        if constexpr (ROTATE) {
-            if (base == 0) {
-                if (threadIdx.x < a.rope.dims / 2)
-                    turns[threadIdx.x] = turn(a.positions[t], a.rope.frequencies[threadIdx.x], a.rope.strength);
+        if (base == 0) {
+            if constexpr (ROTATE) {
+                if (threadIdx.x < pairs) turns[threadIdx.x] = turn(a.positions[t], a.rope.frequencies[threadIdx.x], a.rope.strength);
                 __syncthreads();
+                if (turned) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = turns[4 * c + i];
+                }
             }
+            if (slot >= 0 && slot < a.cache.pages * a.cache.page_size)
+                row0 = (int64_t)(slot / a.cache.page_size) * a.kv_heads * a.cache.page_size + slot % a.cache.page_size;
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int h = base + u * kPer + first;
             if (base + u * kPer >= all) break;      // the same for the whole workgroup
             const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
-            const uint16_t* gamma = is_v ? nullptr : is_q ? a.q_gamma : a.k_gamma;
             float f[8];
-            widen8(raw[u], f);
-            float other[8];   // halves: the other channels of the lane's pairs
-            bool low = false, turned = false;
-            if constexpr (ROTATE && !NEIGHBOURS) {
-                low = c < half;
-                turned = c < 2 * half && !is_v;
-                const int lane = threadIdx.x % kWave;
-                const int from = turned ? (low ? lane + half : lane - half) : lane;
-                v4u o;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = __shfl(raw[u][i], from);
-                widen8(o, other);
-            }
-            if (a.q_gamma || a.k_gamma) {
+            for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(raw[u][i / 2][i % 2]), f[2 * i + 1] = bf16_hi(raw[u][i / 2][i % 2]);
+            float d = 1.0f;   // what remains to be multiplied
+            if (normed) {
                 float squares = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares);
                 squares = lanes_sum<LANES>(squares);
-                if (gamma && mine) {
-                    const float d = 1.0f / sqrtf(squares / (float)a.dim + a.eps);
-                    float w[8];
-                    widen8(*reinterpret_cast<const v4u*>(gamma + 8 * c), w);
+                if (!is_v && (is_q ? a.q_gamma : a.k_gamma)) {
+                    d = __builtin_amdgcn_rsqf(__builtin_fmaf(squares, a.inv_dim, a.eps));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f[i] * w[i] * d;
-                    if constexpr (ROTATE && !NEIGHBOURS) {
-                        if (turned) {
-                            widen8(*reinterpret_cast<const v4u*>(gamma + 8 * (low ? c + half : c - half)), w);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) other[i] = other[i] * w[i] * d;
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t g = is_q ? gamma[0][i / 2][i % 2] : gamma[1][i / 2][i % 2];
+                        f[2 * i] *= bf16_lo(g), f[2 * i + 1] *= bf16_hi(g);
                     }
                 }
             }
-            if constexpr (ROTATE && !NEIGHBOURS) {
-                if (turned) {
-                    const float2* w = turns + 8 * (low ? c : c - half);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f[i] * w[i].x + (low ? -other[i] : other[i]) * w[i].y;
-                }
-            }
-            if constexpr (ROTATE && NEIGHBOURS) {
-                if (c < 2 * half && !is_v) {
+            if constexpr (ROTATE) {
+                if (turned && !is_v) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 w = turns[4 * c + i];
-                        const float x = f[2 * i], y = f[2 * i + 1];
-                        f[2 * i] = x * w.x - y * w.y;
-                        f[2 * i + 1] = y * w.x + x * w.y;
+                        const int m = NEIGHBOURS ? 2 * i : i, n = NEIGHBOURS ? 2 * i + 1 : i + 4;
+                        const float x = f[m], y = f[n];
+                        f[m] = x * w[i].x - y * w[i].y;
+                        f[n] = y * w[i].x + x * w[i].y;
                     }
                 }
             }
@@ -135,71 +128,100 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
                 amax = lanes_max<LANES>(amax);
             }
             if (!mine || h >= all) continue;
-            if (is_q) {
-                *reinterpret_cast<v4u*>(a.q_out + t * a.q_out_stride + h * a.dim + 8 * c) = narrow8(f);
-                continue;
-            }
-            const int head = h - a.heads - (is_v ? a.kv_heads : 0);
-            const int64_t row = ((int64_t)page * a.kv_heads + head) * a.cache.page_size + place;
-            void* codes = is_v ? a.cache.v : a.cache.k;
-            if constexpr (KIND == QLIN_CACHE_BF16) {
-                *reinterpret_cast<v4u*>(static_cast<uint16_t*>(codes) + row * a.dim + 8 * c) = narrow8(f);
-            } else {
+            const int head = is_q ? h : h - a.heads - (is_v ? a.kv_heads : 0);
+            if (is_q || KIND == QLIN_CACHE_BF16) {
+                if (!is_q && row0 < 0) continue;
+                uint16_t* to = is_q ? a.q_out + t * a.q_out_stride + head * a.dim
+                                    : static_cast<uint16_t*>(is_v ? a.cache.v : a.cache.k) + (row0 + (int64_t)head * a.cache.page_size) * a.dim;
+                if (normed) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] *= d;
+                }
+                *reinterpret_cast<v2u*>(to + lo) = v2u{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
+                *reinterpret_cast<v2u*>(to + hi) = v2u{bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
+            } else if (row0 >= 0) {
+                // as in the norm, the codes are those of f: d is left to the scale
                 constexpr bool kFp8 = KIND == QLIN_CACHE_FP8;
-                *reinterpret_cast<v2u*>(static_cast<uint8_t*>(codes) + row * a.dim + 8 * c) = codes8<kFp8>(f, rounding<kFp8>(amax));
-                if (c == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[row] = amax / (kFp8 ? 448.0f : 127.0f);
+                const int64_t row = row0 + (int64_t)head * a.cache.page_size;
+                uint8_t* to = static_cast<uint8_t*>(is_v ? a.cache.v : a.cache.k) + row * a.dim;
+                const v2u codes = codes8<kFp8>(f, rounding<kFp8>(amax));
+                *reinterpret_cast<uint32_t*>(to + lo) = codes.x;
+                *reinterpret_cast<uint32_t*>(to + hi) = codes.y;
+                if (c == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[row] = scale_of<kFp8>(amax * d);
             }
         }
     }
 }
 
-// A workgroup takes `rows` rows of the call; a thread 16 channels of one head
-// of a row, keys and values alike.
+constexpr int kReadAhead = 4;   // rows of a thread whose loads are under way together
+
+// Eight codes times their scale, rounded to bf16.
+template <int KIND>
+__device__ __forceinline__ v4u widen_codes(uint32_t a, uint32_t b, float s) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t d = i ? b : a;
+        if constexpr (KIND == QLIN_CACHE_FP8) {
+            const v2f lo = e4m3_unpack2<false>(d), hi = e4m3_unpack2<true>(d);
+            f[4 * i] = lo.x * s, f[4 * i + 1] = lo.y * s, f[4 * i + 2] = hi.x * s, f[4 * i + 3] = hi.y * s;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[4 * i + j] = (float)(int8_t)(d >> (8 * j)) * s;
+        }
+    }
+    return narrow8(f);
+}
+
+// A thread takes eight channels of a head, of its keys and its values, in every
+// `step`-th row of the workgroup's.
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(qlin_kv_cache a, const int* __restrict__ slots, int64_t n, int rows,
                                                               uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-    const unsigned parts = a.dim / 16, per_row = a.kv_heads * parts;
-    const int64_t first = (int64_t)blockIdx.x * rows;
-    const int64_t total = a.pages * a.page_size;
-    for (unsigned i = threadIdx.x; i < rows * per_row; i += kThreads) {
-        const unsigned r = i / per_row, rest = i - r * per_row, head = rest / parts, part = rest - head * parts;
-        const int64_t at = first + r;
-        if (at >= n) break;
-        const int slot = slots[at];
-        if (slot < 0 || slot >= total) continue;
-        const int page = slot / a.page_size, place = slot % a.page_size;
-        const int64_t row = ((int64_t)page * a.kv_heads + head) * a.page_size + place;
-        const int64_t from = row * a.dim + 16 * part, to = (at * a.kv_heads + head) * a.dim + 16 * part;
-        if constexpr (KIND == QLIN_CACHE_BF16) {
-            const v4u* ks = reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(a.k) + from);
-            const v4u* vs = reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(a.v) + from);
-            const v4u k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
-            v4u *kt = reinterpret_cast<v4u*>(k + to), *vt = reinterpret_cast<v4u*>(v + to);
-            kt[0] = k0, kt[1] = k1, vt[0] = v0, vt[1] = v1;
-        } else {
-            const v4u kw = *reinterpret_cast<const v4u*>(static_cast<const uint8_t*>(a.k) + from);
-            const v4u vw = *reinterpret_cast<const v4u*>(static_cast<const uint8_t*>(a.v) + from);
-            const float ks = a.k_scale[row], vs = a.v_scale[row];
-            auto widen = [](const v4u& w, float s, uint16_t* to) {
-                float f[8];
+    constexpr int kBytes = KIND == QLIN_CACHE_BF16 ? 16 : 8;   // of eight channels
+    const int parts = a.dim / 8, per_row = a.kv_heads * parts;
+    const int across = per_row < kThreads ? per_row : kThreads, step = kThreads / across;
+    const int r0 = threadIdx.x / across;
+    const int64_t first = (int64_t)blockIdx.x * rows, last = first + rows < n ? first + rows : n;
+    const int total = (int)(a.pages * a.page_size);
+    if (r0 >= step) return;
+    for (int i = threadIdx.x - r0 * across; i < per_row; i += across) {
+        const int head = i / parts, part = i - head * parts;
+        for (int64_t at = first + r0; at < last; at += kReadAhead * step) {
+            v4u kw[kReadAhead], vw[kReadAhead];
+            float ks[kReadAhead], vs[kReadAhead];
+            bool live[kReadAhead];
+            int slot[kReadAhead];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+            for (int u = 0; u < kReadAhead; ++u) slot[u] = at + u * step < last ? slots[at + u * step] : -1;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t d = w[2 * half + i];
-                        if constexpr (KIND == QLIN_CACHE_FP8) {
-                            const v2f lo = e4m3_unpack2<false>(d), hi = e4m3_unpack2<true>(d);
-                            f[4 * i] = lo.x * s, f[4 * i + 1] = lo.y * s, f[4 * i + 2] = hi.x * s, f[4 * i + 3] = hi.y * s;
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) f[4 * i + b] = (float)(int8_t)(d >> (8 * b)) * s;
-                        }
-                    }
-                    reinterpret_cast<v4u*>(to)[half] = narrow8(f);
+            for (int u = 0; u < kReadAhead; ++u) {
+                live[u] = slot[u] >= 0 && slot[u] < total;
+                if (!live[u]) continue;
+                const int page = slot[u] / a.page_size, place = slot[u] - page * a.page_size;
+                const int64_t row = ((int64_t)page * a.kv_heads + head) * a.page_size + place;
+                const int64_t from = (row * parts + part) * kBytes;
+                if constexpr (KIND == QLIN_CACHE_BF16) {
+                    kw[u] = *reinterpret_cast<const v4u*>(static_cast<const uint8_t*>(a.k) + from);
+                    vw[u] = *reinterpret_cast<const v4u*>(static_cast<const uint8_t*>(a.v) + from);
+                } else {
+                    const v2u x = *reinterpret_cast<const v2u*>(static_cast<const uint8_t*>(a.k) + from);
+                    const v2u y = *reinterpret_cast<const v2u*>(static_cast<const uint8_t*>(a.v) + from);
+                    kw[u].x = x.x, kw[u].y = x.y, vw[u].x = y.x, vw[u].y = y.y;
+                    ks[u] = a.k_scale[row], vs[u] = a.v_scale[row];
                 }
-            };
-            widen(kw, ks, k + to);
-            widen(vw, vs, v + to);
+            }
+#pragma unroll
+            for (int u = 0; u < kReadAhead; ++u) {
+                if (!live[u]) continue;
+                const int64_t to = (at + u * step) * per_row + i;
+                if constexpr (KIND != QLIN_CACHE_BF16) {
+                    kw[u] = widen_codes<KIND>(kw[u].x, kw[u].y, ks[u]);
+                    vw[u] = widen_codes<KIND>(vw[u].x, vw[u].y, vs[u]);
+                }
+                __builtin_nontemporal_store(kw[u], reinterpret_cast<v4u*>(k) + to);
+                __builtin_nontemporal_store(vw[u], reinterpret_cast<v4u*>(v) + to);
+            }
         }
     }
 }
@@ -228,8 +250,8 @@ hipError_t launch_heads(const HeadsCall& c, hipStream_t st) {
 }
 
 hipError_t launch_cache_read(const qlin_kv_cache& cache, const int* slots, int64_t n, uint16_t* k, uint16_t* v, hipStream_t st) {
-    const int per_row = cache.kv_heads * (cache.dim / 16);
-    const int rows = per_row >= 512 ? 1 : 512 / per_row;
+    const int per_row = cache.kv_heads * (cache.dim / 8), step = per_row < kThreads ? kThreads / per_row : 1;
+    const int rows = kReadAhead * step;
     const dim3 grid((unsigned)((n + rows - 1) / rows)), block(kThreads);
     if (cache.kind == QLIN_CACHE_BF16) hipLaunchKernelGGL(cache_read_kernel<QLIN_CACHE_BF16>, grid, block, 0, st, cache, slots, n, rows, k, v);
     else if (cache.kind == QLIN_CACHE_INT8) hipLaunchKernelGGL(cache_read_kernel<QLIN_CACHE_INT8>, grid, block, 0, st, cache, slots, n, rows, k, v);

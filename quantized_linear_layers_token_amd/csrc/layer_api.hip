@@ -146,6 +146,7 @@ qlin_status qlin_rope(const uint16_t* x, int64_t x_stride, const int32_t* positi
     c.rope = *rope;
     c.heads = heads;
     c.dim = dim;
+    c.inv_dim = 1.0f / (float)dim;
     c.T = T;
     return qlin::hip_status(qlin::launch_heads(c, stream));
 }
@@ -207,6 +208,7 @@ qlin_status qlin_cache_write(const qlin_kv_cache* cache, const int32_t* slots, i
     c.cache = *cache;
     c.kv_heads = cache->kv_heads;
     c.dim = dim;
+    c.inv_dim = 1.0f / (float)dim;
     c.T = T;
     return qlin::hip_status(qlin::launch_heads(c, stream));
 }

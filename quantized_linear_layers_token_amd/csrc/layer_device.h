@@ -16,34 +16,63 @@ namespace qlin {
 struct Rounding {
     float pre, inv;
 };
+
+// fl32(1 / a) for 2^-100 < a < 2^126: the hardware's reciprocal (off by one
+// unit at most) and one correction, which rounds it correctly (every mantissa is tested).
+__device__ __forceinline__ float reciprocal(float a) {
+    const float r = __builtin_amdgcn_rcpf(a);
+    return __builtin_fmaf(__builtin_fmaf(-a, r, 1.0f), r, r);
+}
+// fl32(a / Q) for the two ranges, by the reciprocal of Q and a correction (the same).
+template <bool FP8>
+__device__ __forceinline__ float scale_of(float a) {
+    constexpr float q = FP8 ? 448.0f : 127.0f, inv = 1.0f / q;
+    const float r = a * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, r, a), inv, r);
+}
 template <bool FP8>
 __device__ __forceinline__ Rounding rounding(float a) {
     const float q = FP8 ? 448.0f : 127.0f;
     const float pre = a < 0x1p-64f ? 0x1p64f : 1.0f;
-    return Rounding{pre, a == 0.0f ? 0.0f : q * (1.0f / (a * pre))};
+    return Rounding{pre, a == 0.0f ? 0.0f : q * reciprocal(a * pre)};
 }
+// Codes of four values.  Nothing saturates: |t * inv| exceeds Q by two units of
+// f32 at most, which round to Q.  int8: adding 1.5 * 2^23 rounds to an integer,
+// ties to even, and leaves it in the low byte.
 template <bool FP8>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, Rounding r) {
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+#pragma clang fp contract(off)
     if constexpr (FP8) {
-        auto t = [r](float v) { return fminf(fmaxf((v * r.pre) * r.inv, -448.0f), 448.0f); };
-        return e4m3_pack_hi(e4m3_pack_lo(t(a), t(b)), t(c), t(d));
+        return e4m3_pack_hi(e4m3_pack_lo(a * inv, b * inv), c * inv, d * inv);
     } else {
-        auto t = [r](float v) {
-            return (uint32_t)(uint8_t)(int8_t)(int)fminf(fmaxf(__builtin_rintf((v * r.pre) * r.inv), -127.0f), 127.0f);
+        constexpr float magic = 12582912.0f;
+        auto t = [inv](float v) {
+#pragma clang fp contract(off)
+            const float x = v * inv;
+            return __float_as_uint(x + magic);
         };
-        return t(a) | (t(b) << 8) | (t(c) << 16) | (t(d) << 24);
+        const uint32_t lo = __builtin_amdgcn_perm(t(b), t(a), 0x0C0C0400), hi = __builtin_amdgcn_perm(t(d), t(c), 0x04000C0C);
+        return lo | hi;
     }
 }
 template <bool FP8>
-__device__ __forceinline__ v2u codes8(const float (&t)[8], Rounding r) {
-    return v2u{codes4<FP8>(t[0], t[1], t[2], t[3], r), codes4<FP8>(t[4], t[5], t[6], t[7], r)};
+__device__ __forceinline__ v2u codes8(float (&t)[8], Rounding r) {
+    if (r.pre != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] *= r.pre;
+    }
+    return v2u{codes4<FP8>(t[0], t[1], t[2], t[3], r.inv), codes4<FP8>(t[4], t[5], t[6], t[7], r.inv)};
 }
 
 __device__ __forceinline__ void widen8(const v4u& v, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(v[i]), f[2 * i + 1] = bf16_hi(v[i]);
 }
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) { return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16); }
+// Two values rounded to bf16 (one instruction).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, v2bf{(__bf16)a, (__bf16)b});
+}
 __device__ __forceinline__ v4u narrow8(const float (&f)[8]) {
     return v4u{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
 }

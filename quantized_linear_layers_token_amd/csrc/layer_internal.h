@@ -33,7 +33,7 @@ struct HeadsCall {
     uint16_t* q_out;
     int64_t q_out_stride;
     const uint16_t *q_gamma, *k_gamma;   // or null
-    float eps;
+    float eps, inv_dim;
     const int* positions;
     const int* slots;
     qlin_rotation rope;                  // frequencies null: no rotation

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
     Rounding rr = {};
     if constexpr (OUT == kNormInt8 || OUT == kNormFp8) {
         rr = rounding<kFp8>(amax);
-        if (tid == 0) a.s[m] = amax * d / (kFp8 ? 448.0f : 127.0f);
+        if (tid == 0) a.s[m] = scale_of<kFp8>(amax * d);
     }
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
         } else {
             if constexpr (OUT == kNormFp8Block) {
                 rr = rounding<true>(group[j]);
-                if (c % 16 == 0) a.s[m * (a.K / 128) + c / 16] = group[j] * d / 448.0f;
+                if (c % 16 == 0) a.s[m * (a.K / 128) + c / 16] = scale_of<true>(group[j] * d);
             }
             reinterpret_cast<v2u*>(static_cast<uint8_t*>(a.y) + m * a.K)[c] = codes8<kFp8>(f, rr);
         }
