@@ -43,7 +43,8 @@ struct AttnArgs {
     const float *k_scale, *v_scale;
     const int *pages, *lengths;
     uint16_t* out;
-    float* sums;      // partial sums [group of heads][worker][2][rows][dim + 2]
+    float* sums;      // partial sums [group of heads][worker][2][rows][dim]
+    float* stats;     // their maxima and sums of p [group of heads][worker][2][rows][2]
     int* joins;       // [group of heads][worker][3]: sequence (-1: none), its last worker, the part of the first
     int64_t npages;
     int S, heads, kv_heads, dim, columns, page_size, window;
@@ -134,56 +135,65 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&to)[N])
     }
 }
 
-template <int KIND, int DP>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
+// Inclusive sums over the wavefront's lanes (each at most 2^25: no overflow).
+__device__ __forceinline__ unsigned scan(unsigned v) {
+    auto add = [](unsigned v, unsigned o) { return v + o; };
+    v = add(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));
+    v = add(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+    v = add(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+    v = add(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+    v = add(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // lane 15 (47) to the next row
+    v = add(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // lane 31 to the upper rows
+    return v;
+}
+__device__ __forceinline__ unsigned lane_of(unsigned v, int lane) { return (unsigned)__builtin_amdgcn_readlane((int)v, lane); }
+
+// ALONE: a workgroup takes a whole sequence, and nothing is joined.
+template <int KIND, int DP, int WAVES, bool ALONE>
+__global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
     using T = Tiles<KIND, DP>;
     constexpr int kTiles = DP / 16, kSteps = DP / 32;
     constexpr int kPad = DP + 4;
-    __shared__ float joined[2][kAttnHeads * kPad];
-    __shared__ float stats[2][2][kAttnHeads];
+    __shared__ float joined[WAVES / 2][kAttnHeads * kPad];
+    __shared__ float stats[WAVES / 2][2][kAttnHeads];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
-    const int group = blockIdx.x % (a.kv_heads * a.tiles), worker = blockIdx.x / (a.kv_heads * a.tiles);
+    const int groups = a.kv_heads * a.tiles;
+    const int group = blockIdx.x % groups, worker = blockIdx.x / groups;
     const int kv_head = group / a.tiles, tile = group % a.tiles;
     const int shared_by = a.heads / a.kv_heads;
     const int head0 = kv_head * shared_by + tile * kAttnHeads;
     const int rows = min(a.rows, shared_by - tile * kAttnHeads);
-    int* join = a.joins + ((int64_t)group * a.workers + worker) * 3;
+    int* join = ALONE ? nullptr : a.joins + ((int64_t)group * a.workers + worker) * 3;
 
-    // sequences without tokens, a share of them each
-    for (int s = worker * kWaves + wave; s < a.S; s += a.workers * kWaves)
-        if (a.lengths[s] == 0 || a.columns == 0)
-            if (a.lengths[s] >= 0)
-                for (int i = lane; i < rows * a.dim / 2; i += kWave)
-                    reinterpret_cast<uint32_t*>(a.out + ((int64_t)s * a.heads + head0) * a.dim)[i] = 0;
-
-    // the worker's units, and the sequence of the first of them
-    int64_t total = 0;
-    for (int s = lane; s < a.S; s += kWave) total += span_of(a.lengths[s], a).units;
-#pragma unroll
-    for (int m = 1; m < kWave; m *= 2) total += __shfl_xor(total, m);
-    const int64_t share = attn_share(total, a.workers);
-    const int64_t lo = worker * share, hi = min(lo + share, total);
-    if (threadIdx.x == 0) join[0] = -1;
-    if (lo >= total) return;
     int s = 0;
-    int64_t before = 0;   // units of the sequences before s
-    for (int c = 0; c < a.S; c += kWave) {
-        const unsigned u = c + lane < a.S ? span_of(a.lengths[c + lane], a).units : 0;
-        unsigned upto = u;
-#pragma unroll
-        for (int m = 1; m < kWave; m *= 2) {
-            const unsigned o = __shfl_up(upto, m);
-            upto += lane >= m ? o : 0;
+    int64_t before = 0, lo = 0, hi = 0, share = 0;   // units of the sequences before s; the workgroup's first and end; of each workgroup
+    if constexpr (ALONE) {
+        s = worker;
+        hi = span_of(table_of(a.lengths)[s], a).units;
+    } else {
+        // the worker's units, and the sequence of the first of them
+        auto units_at = [&](int first) { return first + lane < a.S ? span_of(a.lengths[first + lane], a).units : 0; };
+        unsigned units = units_at(0), upto = scan(units);
+        int64_t total = lane_of(upto, kWave - 1);
+        for (int c = kWave; c < a.S; c += kWave) total += lane_of(scan(units_at(c)), kWave - 1);
+        share = attn_share(total, a.workers);
+        lo = worker * share, hi = lo < total ? min(lo + share, total) : 0;
+        if (threadIdx.x == 0) join[0] = -1;
+        if (lo < total) {
+            for (int c = 0;;) {
+                const uint64_t past = __ballot(before + upto > lo);
+                if (past) {
+                    const int at = __builtin_ctzll(past);
+                    s = c + at;
+                    before += lane_of(upto - units, at);
+                    break;
+                }
+                before += lane_of(upto, kWave - 1);
+                c += kWave;
+                units = units_at(c), upto = scan(units);
+            }
         }
-        const uint64_t past = __ballot(before + upto > lo);
-        if (past) {
-            const int at = __builtin_ctzll(past);
-            s = c + at;
-            before += (unsigned)__builtin_amdgcn_readlane((int)(upto - u), at);
-            break;
-        }
-        before += (unsigned)__builtin_amdgcn_readlane((int)upto, kWave - 1);
     }
 
     const int64_t row_bytes = (int64_t)a.dim * T::kBytes;
@@ -197,14 +207,14 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnA
     const int value_piece = n * (DP / 16 * T::kBytes);
     const int value_at = 4 * g * (int)row_bytes + (value_piece < row_bytes ? value_piece : 0);
 
-    for (; s < a.S && before < hi; ++s) {
+    for (; before < hi; ++s) {   // (hi is at most the units of all: the loop ends before s leaves the batch)
         s = __builtin_amdgcn_readfirstlane(s);
         const AttnSpan span = span_of(table_of(a.lengths)[s], a);
         if (span.units == 0) continue;
         const int first = (int)(max(lo, before) - before), last = (int)(min(hi, before + span.units) - before);
         // the wavefront's units of them
-        const int mine = first + (int)((int64_t)(last - first) * wave / kWaves);
-        const int end = first + (int)((int64_t)(last - first) * (wave + 1) / kWaves);
+        const int mine = first + (int)((int64_t)(last - first) * wave / WAVES);
+        const int end = first + (int)((int64_t)(last - first) * (wave + 1) / WAVES);
 
         v8bf q[kSteps];
 #pragma unroll
@@ -367,8 +377,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnA
         settle();
         l = column_sum(l);
 
-        // The four wavefronts' sums, joined in pairs: 2 and 3 hand theirs to 0
-        // and 1, then 1 to 0.  acc[r][i] is channel (DP / 16) (4 g + i) + r of head n.
+        // The wavefronts' sums, joined in pairs: the upper half hands its to the
+        // lower, and so on.  acc[r][i] is channel (DP / 16) (4 g + i) + r of head n.
         auto give = [&](int slot) {
             if (n < rows) {
                 float* to = joined[slot] + n * kPad + 4 * g * kTiles;
@@ -394,19 +404,18 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnA
                 m = now;
             }
         };
-        __syncthreads();   // the buffers are free
-        if (wave >= 2) give(wave - 2);
-        __syncthreads();
-        if (wave < 2) take(wave);
-        __syncthreads();
-        if (wave == 1) give(0);
-        __syncthreads();
-        if (wave == 0) take(0);
+#pragma unroll
+        for (int half = WAVES / 2; half >= 1; half /= 2) {
+            __syncthreads();   // the buffers are free
+            if (wave >= half && wave < 2 * half) give(wave - half);
+            __syncthreads();
+            if (wave < half) take(wave);
+        }
 
         const bool starts = before >= lo, ends = before + span.units <= hi;
         if (wave == 0 && n < rows) {
             const int d0 = 4 * g * kTiles;
-            if (starts && ends) {
+            if (ALONE || (starts && ends)) {
                 const float by = l > 0.0f || l != l ? 1.0f / l : 0.0f;
                 uint16_t* to = a.out + ((int64_t)s * a.heads + head0 + n) * a.dim + d0;
 #pragma unroll
@@ -418,14 +427,15 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnA
                 }
             } else {
                 const int part = attn_part(before, lo);
-                float* to = a.sums + ((((int64_t)group * a.workers + worker) * 2 + part) * a.rows + n) * (a.dim + 2);
-                if (g == 0) to[0] = m, to[1] = l;
+                const int64_t at = (((int64_t)group * a.workers + worker) * 2 + part) * a.rows + n;
+                float* to = a.sums + at * a.dim + d0;
+                if (g == 0) *reinterpret_cast<v2f*>(a.stats + 2 * at) = v2f{m, l};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                    for (int r = 0; r < kTiles; r += 2)
+                    for (int r = 0; r < kTiles; r += 4)
                         if (d0 + i * kTiles + r < a.dim)
-                            *reinterpret_cast<v2f*>(to + 2 + d0 + i * kTiles + r) = v2f{acc[r][i], acc[r + 1][i]};
+                            *reinterpret_cast<v4f*>(to + i * kTiles + r) = v4f{acc[r][i], acc[r + 1][i], acc[r + 2][i], acc[r + 3][i]};
                 }
                 if (starts && lane == 0) {
                     join[0] = s;
@@ -436,70 +446,94 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_kernel(AttnA
         }
         before += span.units;
     }
+
+    // sequences without tokens: zeros, a share of them for each workgroup
+    for (int e = worker * WAVES + wave; e < (ALONE ? (wave == 0 ? worker * WAVES + 1 : 0) : a.S); e += a.workers * WAVES) {
+        const int of = ALONE ? worker : e, length = table_of(a.lengths)[of];
+        if (length == 0 || (length > 0 && a.columns == 0))
+            for (int i = lane; i < rows * a.dim / 2; i += kWave)
+                reinterpret_cast<uint32_t*>(a.out + ((int64_t)of * a.heads + head0) * a.dim)[i] = 0;
+    }
 }
 
 // A workgroup joins the parts of the sequence that began with a worker and went
-// on, for one query head: the wavefronts take every fourth part.
+// on, a wavefront one query head at a time: lane p holds the maximum and the
+// sum of part p, the values of eight parts are under way together.
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
-    __shared__ float part_max[kWaves], part_sum[kWaves];
-    __shared__ float part_out[kWaves][QLIN_MAX_HEAD_DIM];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int worker = blockIdx.x % a.workers, at = blockIdx.x / a.workers;
-    const int group = at / a.rows, row = at % a.rows;
-    const int* join = a.joins + ((int64_t)group * a.workers + worker) * 3;
-    const int s = join[0];
+    constexpr int kTogether = 8;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int groups = a.kv_heads * a.tiles;
+    const int group = blockIdx.x % groups, worker = blockIdx.x / groups;
+    const Table join = table_of(a.joins + ((int64_t)group * a.workers + worker) * 3);
+    const int s = join[0], last = join[1], part = join[2];
+    if (s < 0) return;
     const int shared_by = a.heads / a.kv_heads, tile = group % a.tiles;
-    if (s < 0 || tile * kAttnHeads + row >= shared_by) return;
-    const int last = join[1], part = join[2];
-    auto sums = [&](int w) {
-        return a.sums + ((((int64_t)group * a.workers + w) * 2 + (w == worker ? part : 0)) * a.rows + row) * (a.dim + 2);
+    const int rows = min(a.rows, shared_by - tile * kAttnHeads);
+    const int parts = last - worker + 1;
+    auto record = [&](int p, int row) {   // part p: the first lies in `part`, the others over their worker's first unit
+        return (((int64_t)group * a.workers + worker + p) * 2 + (p == 0 ? part : 0)) * a.rows + row;
     };
-    // each wavefront keeps a running maximum of its own
-    float m = kNone, l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int w = worker + wave; w <= last; w += kWaves) {
-        const float* p = sums(w);
-        const float pm = p[0], pl = p[1];
-        v2f x[2];
+    for (int row = wave; row < rows; row += kWaves) {
+        float m = kNone, l = 0.0f, o[4] = {0, 0, 0, 0};
+        for (int p0 = 0; p0 < parts; p0 += kWave) {
+            v2f mine = v2f{kNone, 0.0f};
+            if (p0 + lane < parts) mine = *reinterpret_cast<const v2f*>(a.stats + 2 * record(p0 + lane, row));
+            const int here = min(parts - p0, kWave);
+            float top = lanes_max<16>(mine.x);
+            top = fmaxf(m, column_max(top));
+            const float zero_at = top == kNone ? 0.0f : top;
+            const float weight = __builtin_amdgcn_exp2f(mine.x - zero_at), by = __builtin_amdgcn_exp2f(m - zero_at);
+            l = l * by + column_sum(lanes_sum<16>(mine.y * weight));
+            m = top;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= by;
+            for (int p = 0; p < here; p += kTogether) {
+                v2f x[kTogether][2];
+#pragma unroll
+                for (int u = 0; u < kTogether; ++u) {
+                    const float* from = a.sums + record(p0 + min(p + u, here - 1), row) * a.dim;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int d = 2 * lane + 128 * i;
+                        x[u][i] = d < a.dim ? *reinterpret_cast<const v2f*>(from + d) : v2f{0, 0};
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kTogether; ++u) {
+                    const float w = p + u < here ? __uint_as_float(lane_of(__float_as_uint(weight), min(p + u, kWave - 1))) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[u][i / 2][i % 2], w, o[i]);
+                }
+            }
+        }
+        const float by = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        const int head = group / a.tiles * shared_by + tile * kAttnHeads + row;
+        uint16_t* to = a.out + ((int64_t)s * a.heads + head) * a.dim;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int d = 2 * lane + 128 * i;
-            x[i] = d < a.dim ? *reinterpret_cast<const v2f*>(p + 2 + d) : v2f{0, 0};
+            if (d < a.dim) *reinterpret_cast<uint32_t*>(to + d) = bf16_pair(o[2 * i] * by, o[2 * i + 1] * by);
         }
-        const float now = fmaxf(m, pm), zero_at = now == kNone ? 0.0f : now;
-        const float by = __builtin_amdgcn_exp2f(m - zero_at), other = __builtin_amdgcn_exp2f(pm - zero_at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * by + x[i / 2][i % 2] * other;
-        l = l * by + pl * other;
-        m = now;
     }
-    if (lane == 0) part_max[wave] = m, part_sum[wave] = l;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part_out[wave][2 * lane + 128 * (i / 2) + i % 2] = o[i];
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d >= a.dim) return;
-    float top = kNone;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, part_max[w]);
-    top = top == kNone ? 0.0f : top;
-    float sum = 0.0f, out = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const float by = __builtin_amdgcn_exp2f(part_max[w] - top);
-        sum += part_sum[w] * by;
-        out += part_out[w][d] * by;
-    }
-    const int head = group / a.tiles * shared_by + tile * kAttnHeads + row;
-    a.out[((int64_t)s * a.heads + head) * a.dim + d] = f32_to_bf16(sum > 0.0f || sum != sum ? out / sum : 0.0f);
 }
 
+template <int KIND, int DP>
+void launch_dim(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
+    constexpr int kAlone = DP == 256 ? kWaves : 8;   // (heads of 256 channels take the registers of a SIMD for one wavefront)
+    if (alone) hipLaunchKernelGGL((attn_kernel<KIND, DP, kAlone, true>), dim3(grid), dim3(kAlone * kWave), 0, st, a);
+    else hipLaunchKernelGGL((attn_kernel<KIND, DP, kWaves, false>), dim3(grid), dim3(kThreads), 0, st, a);
+}
 template <int KIND>
-void launch_kind(const AttnArgs& a, unsigned grid, hipStream_t st) {
-    if (a.dim <= 64) hipLaunchKernelGGL((attn_kernel<KIND, 64>), dim3(grid), dim3(kThreads), 0, st, a);
-    else if (a.dim <= 128) hipLaunchKernelGGL((attn_kernel<KIND, 128>), dim3(grid), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((attn_kernel<KIND, 256>), dim3(grid), dim3(kThreads), 0, st, a);
+void launch_kind(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
+    if (a.dim <= 64) launch_dim<KIND, 64>(a, alone, grid, st);
+    else if (a.dim <= 128) launch_dim<KIND, 128>(a, alone, grid, st);
+    else launch_dim<KIND, 256>(a, alone, grid, st);
 }
 
+// Tables of up to this many tokens a sequence take a workgroup for each sequence
+// and one launch.
+constexpr int64_t kAloneTokens = 2048;
+constexpr int64_t kMaxGrid = int64_t(1) << 22;   // workgroups of 512 threads: a launch holds 2^32 threads
 constexpr int kResident = 512;   // workgroups of four wavefronts that the card holds at once: two on each CU
 
 }  // namespace
@@ -530,7 +564,9 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.lengths = c.lengths;
     a.out = c.out;
     a.sums = static_cast<float*>(c.workspace);
-    a.joins = reinterpret_cast<int*>(a.sums + (int64_t)groups * shape.workers * 2 * shape.rows * (c.cache.dim + 2));
+    const int64_t records = (int64_t)groups * shape.workers * 2 * shape.rows;
+    a.stats = a.sums + records * c.cache.dim;
+    a.joins = reinterpret_cast<int*>(a.stats + records * 2);
     a.npages = c.cache.pages;
     a.S = c.S;
     a.heads = c.heads;
@@ -543,13 +579,15 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.rows = shape.rows;
     a.workers = shape.workers;
     a.scale = c.scale * 1.44269504088896340736f;
-    const unsigned grid = (unsigned)(groups * shape.workers);
-    if (c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(a, grid, st);
-    else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(a, grid, st);
-    else launch_kind<QLIN_CACHE_FP8>(a, grid, st);
+    // (64-bit: S times the groups of heads)
+    const bool alone = (int64_t)c.columns * c.cache.page_size <= kAloneTokens && (int64_t)c.S * groups <= kMaxGrid;
+    const unsigned grid = (unsigned)(alone ? (int64_t)c.S * groups : (int64_t)groups * shape.workers);
+    if (c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(a, alone, grid, st);
+    else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(a, alone, grid, st);
+    else launch_kind<QLIN_CACHE_FP8>(a, alone, grid, st);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && shape.workers > 1) {
-        hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(groups * shape.rows * shape.workers)), dim3(kThreads), 0, st, a);
+    if (e == hipSuccess && !alone && shape.workers > 1) {
+        hipLaunchKernelGGL(attn_join_kernel, dim3(grid), dim3(kThreads), 0, st, a);
         e = hipGetLastError();
     }
     return e;

@@ -17,13 +17,9 @@ struct Rounding {
     float pre, inv;
 };
 
-// fl32(1 / a) for 2^-100 < a < 2^126: the hardware's reciprocal (off by one
-// unit at most) and one correction, which rounds it correctly (every mantissa is tested).
-__device__ __forceinline__ float reciprocal(float a) {
-    const float r = __builtin_amdgcn_rcpf(a);
-    return __builtin_fmaf(__builtin_fmaf(-a, r, 1.0f), r, r);
-}
-// fl32(a / Q) for the two ranges, by the reciprocal of Q and a correction (the same).
+// fl32(a / Q) by the reciprocal of Q and one correction: correctly rounded for
+// every mantissa of a and both ranges (1 / a takes a division: the same two
+// steps from the hardware's reciprocal miss the last bit of 33 mantissas).
 template <bool FP8>
 __device__ __forceinline__ float scale_of(float a) {
     constexpr float q = FP8 ? 448.0f : 127.0f, inv = 1.0f / q;
@@ -34,7 +30,7 @@ template <bool FP8>
 __device__ __forceinline__ Rounding rounding(float a) {
     const float q = FP8 ? 448.0f : 127.0f;
     const float pre = a < 0x1p-64f ? 0x1p64f : 1.0f;
-    return Rounding{pre, a == 0.0f ? 0.0f : q * reciprocal(a * pre)};
+    return Rounding{pre, a == 0.0f ? 0.0f : q * (1.0f / (a * pre))};
 }
 // Codes of four values.  Nothing saturates: |t * inv| exceeds Q by two units of
 // f32 at most, which round to Q.  int8: adding 1.5 * 2^23 rounds to an integer,

@@ -88,6 +88,17 @@ def test_attention_indices_in_host_code(tmp_path):
     assert r.returncode == 0 and "every bound held" in r.stdout, r.stdout + r.stderr
 
 
+def test_scales_are_correctly_rounded(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ is not installed")
+    exe = str(tmp_path / "rounding_check")
+    r = subprocess.run(["g++", "-std=c++17", "-O2", "-mfma", "-ffp-contract=off", os.path.join(HC, "rounding_check.cpp"), "-o", exe],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.strip() == "0 differ", r.stdout
+
+
 def t(*shape, dtype=torch.int16):
     return torch.zeros(shape, dtype=dtype)
 

@@ -1,4 +1,4 @@
-"""The corrected reciprocals behind the norm's and the cache's codes and scales: every mantissa of an absmax."""
+"""Codes and scales of the norm and the cache over the mantissas of an absmax that bf16 rows and products give."""
 import numpy as np
 import pytest
 
