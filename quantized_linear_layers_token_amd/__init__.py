@@ -587,42 +587,78 @@ def qlin_experts_w4(x, ids, weights, gate, up, down, y, workspace, stream=None):
 import math as _math  # noqa: E402
 
 
-def _norm_args(x, gamma, residual, sum_out):
-    """-> (device, M, K) after the checks that the norms share."""
-    device, M, K = _w4_input(x)
-    _w4_tensor(gamma, "gamma", (K,), 2, device)
-    if (residual is None) != (sum_out is None):
+# Host time of a call weighs as much as a decode step's launch: these check a tensor in one go (its device by number) and
+# say what is wrong only where something is.
+_BYTE, _TWO = _TYPES[1], _TYPES[2]
+_INT32, _FLOAT32 = frozenset([_torch.int32]), frozenset([_torch.float32])
+
+
+def _expect(t, name, types, shape, index):
+    """t is a contiguous tensor of this shape (None: any) and one of these types, on device number `index` (-1: the host)."""
+    if t.dtype in types and (shape is None or t.shape == shape) and t.get_device() == index and t.is_contiguous():
+        return
+    if types is _INT32 or types is _FLOAT32:
+        if t.dtype not in types:
+            raise ValueError(f"{name} must be {'int32' if types is _INT32 else 'float32'}, not {t.dtype}")
+    _w4_tensor(t, name, shape, {_BYTE: 1, _TWO: 2}.get(types, 4), t.device)
+    raise ValueError(f"{name} is on {t.device}, the call runs on device {index}")
+
+
+def _launch_on(fn, index, stream, *args):
+    if index < 0:
+        raise ValueError("the tensors must be device tensors")
+    if stream is None:
+        stream = _raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if index == _current_device():
+        status = fn(*args, stream)
+    else:
+        with _torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != QLIN_OK:
+        raise QlinError(status, fn.__name__)
+
+
+def _norm(fn, x, gamma, outputs, group, residual, sum_out, eps, stream):
+    """The three norms: outputs are (y,) or (q, s)."""
+    if x.dtype not in _TWO or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D tensor of bfloat16 (or its bit patterns)")
+    index, shape = x.get_device(), x.shape
+    M, K = shape
+    _expect(gamma, "gamma", _TWO, (K,), index)
+    if len(outputs) == 1:
+        _expect(outputs[0], "y", _TWO, shape, index)
+    else:
+        _expect(outputs[0], "q", _BYTE, shape, index)
+        _expect(outputs[1], "s", _FLOAT32, (M, K // 128) if group == 128 else (M,), index)
+    if residual is not None and sum_out is not None:
+        _expect(residual, "residual", _TWO, shape, index)
+        if sum_out is not residual:
+            _expect(sum_out, "sum_out", _TWO, shape, index)
+        r, total = residual.data_ptr(), sum_out.data_ptr()
+    elif residual is None and sum_out is None:
+        r = total = None
+    else:
         raise ValueError("residual and sum_out come together")
-    if residual is not None:
-        _w4_tensor(residual, "residual", (M, K), 2, device)
-        _w4_tensor(sum_out, "sum_out", (M, K), 2, device)
-    return device, M, K
+    more = () if group is None else (group,)
+    _launch_on(fn, index, stream, x.data_ptr(), r, gamma.data_ptr(), M, K, eps, *more, total, *[t.data_ptr() for t in outputs])
 
 
 def qlin_norm_bf16(x, gamma, y, residual=None, sum_out=None, eps=1e-6, stream=None):
     """x bf16 [M, K]; gamma bf16 [K]; y bf16 [M, K] receives the RMS norm of x, or of x + residual, which goes to
     sum_out (both bf16 [M, K]; sum_out may be residual itself)."""
-    device, M, K = _norm_args(x, gamma, residual, sum_out)
-    _w4_tensor(y, "y", (M, K), 2, device)
-    _launch(_lib.qlin_norm_bf16, device, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, K, eps, _ptr(sum_out), y.data_ptr())
+    _norm(_lib.qlin_norm_bf16, x, gamma, (y,), None, residual, sum_out, eps, stream)
 
 
 def qlin_norm_int8(x, gamma, q, s, residual=None, sum_out=None, eps=1e-6, stream=None):
-    """qlin_norm_bf16 rounded as qlin_quant_act_int8 does, in one launch: q int8 [M, K], s f32 [M]."""
-    device, M, K = _norm_args(x, gamma, residual, sum_out)
-    _w4_tensor(q, "q", (M, K), 1, device)
-    _w4_tensor(s, "s", (M,), 4, device)
-    _launch(_lib.qlin_norm_int8, device, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, K, eps, _ptr(sum_out), q.data_ptr(),
-            s.data_ptr())
+    """qlin_norm_bf16 rounded for qlin_gemm_w8a8, in one launch: q int8 [M, K], s f32 [M]."""
+    _norm(_lib.qlin_norm_int8, x, gamma, (q, s), None, residual, sum_out, eps, stream)
 
 
 def qlin_norm_fp8(x, gamma, q, s, group=0, residual=None, sum_out=None, eps=1e-6, stream=None):
-    """qlin_norm_bf16 rounded as qlin_quant_act_fp8 does: q E4M3 codes [M, K], s f32 [M] (group 0) or [M, K/128] (group 128)."""
-    device, M, K = _norm_args(x, gamma, residual, sum_out)
-    _w4_tensor(q, "q", (M, K), 1, device)
-    _w4_tensor(s, "s", (M, K // 128) if group == 128 else (M,), 4, device)
-    _launch(_lib.qlin_norm_fp8, device, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, K, eps, group, _ptr(sum_out), q.data_ptr(),
-            s.data_ptr())
+    """qlin_norm_bf16 rounded for qlin_gemm_fp8_*: q E4M3 codes [M, K], s f32 [M] (group 0) or [M, K/128] (group 128)."""
+    _norm(_lib.qlin_norm_fp8, x, gamma, (q, s), group, residual, sum_out, eps, stream)
 
 
 class _Fixed:
@@ -658,7 +694,7 @@ class Rope(_Fixed):
         if frequencies.dtype is not _torch.float64 or frequencies.shape != (dims // 2,) or not frequencies.is_contiguous():
             raise ValueError(f"frequencies must be a contiguous float64 tensor of {dims // 2}")
         strength = default if strength is None else float(strength)
-        vars(self).update(frequencies=frequencies, dims=dims, interleaved=bool(interleaved), strength=strength, device=frequencies.device,
+        vars(self).update(frequencies=frequencies, dims=dims, interleaved=bool(interleaved), strength=strength, device=frequencies.device, _index=frequencies.get_device(),
                           _bytes=bytes(QlinRotation(frequencies.data_ptr(), dims, 1 if interleaved else 0, strength)))
 
     @staticmethod
@@ -723,7 +759,7 @@ class KVCache(_Fixed):
         if max(pages, kv_heads, page_size, dim) > 0x7fffffff:
             raise QlinError(QLIN_ERR_SHAPE, "KVCache")
         vars(self).update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, pages=pages, kv_heads=kv_heads, page_size=page_size, dim=dim, kind=kind,
-                          device=device, _workspaces={}, _bytes=bytes(QlinKVCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages, kv_heads,
+                          device=device, _index=k.get_device(), _workspaces={}, _bytes=bytes(QlinKVCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages, kv_heads,
                                                                   page_size, dim, kind)))
 
     @classmethod
@@ -740,42 +776,39 @@ class KVCache(_Fixed):
         return KVCache, (self.k, self.v, self.k_scale, self.v_scale)
 
 
-def _heads(t, name, heads, dim, device, T=None):
+def _heads(t, name, T, heads, dim, index):
     """-> stride between the tokens of t, bf16 [T, heads, dim] with contiguous heads and any stride between tokens."""
-    if t.dtype not in _TYPES[2] or t.dim() != 3 or t.device != device:
+    if t.dtype not in _TWO or t.dim() != 3 or t.get_device() != index:
         if t.dtype is _torch.float16:
             raise ValueError(f"{name} must be bfloat16 (or its bit patterns), not float16")
-        raise ValueError(f"{name} must be a 3-D tensor of 2-byte elements on {device}")
-    n, h, d = t.shape
-    if h != heads or d != dim or (T is not None and n != T):
-        raise ValueError(f"{name} must be [{'T' if T is None else T}, {heads}, {dim}], not {list(t.shape)}")
+        raise ValueError(f"{name} must be a 3-D tensor of 2-byte elements on the call's device, not {t.dtype} {list(t.shape)} on {t.device}")
+    if t.shape != (T, heads, dim):
+        raise ValueError(f"{name} must be {[T, heads, dim]}, not {list(t.shape)}")
     between, inner, last = t.stride()
-    if (last != 1 and d > 1) or (inner != d and h > 1):
+    if (last != 1 and dim > 1) or (inner != dim and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return between if n > 1 else h * d
+    return between if T > 1 else heads * dim
 
 
-def _int32(t, name, shape, device):
-    if t.dtype is not _torch.int32:
-        raise ValueError(f"{name} must be int32 {list(shape)}")
-    _w4_tensor(t, name, shape, 4, device)
+def _rope_bytes(rope, positions, T, index):
+    _expect(positions, "positions", _INT32, (T,), index)
+    if rope._index != index:
+        raise ValueError(f"rope is on {rope.device}, the call runs on device {index}")
+    return rope._bytes
 
 
 def qlin_rope(x, positions, rope, y, gamma=None, eps=1e-6, stream=None):
     """x bf16 [T, heads, dim] (any stride between tokens); positions int32 [T]; y like x, may be x, receives the rotated
     heads.  gamma bf16 [dim]: each head's RMS norm first."""
-    device = x.device
     if x.dim() != 3:
         raise ValueError("x must be [T, heads, dim]")
+    index = x.get_device()
     T, heads, dim = x.shape
-    xs, ys = _heads(x, "x", heads, dim, device), _heads(y, "y", heads, dim, device, T)
-    _int32(positions, "positions", (T,), device)
+    xs, ys = _heads(x, "x", T, heads, dim, index), _heads(y, "y", T, heads, dim, index)
+    turn = _rope_bytes(rope, positions, T, index)
     if gamma is not None:
-        _w4_tensor(gamma, "gamma", (dim,), 2, device)
-    if rope.device != device:
-        raise ValueError(f"rope is on {rope.device}, the call runs on {device}")
-    _launch(_lib.qlin_rope, device, stream, x.data_ptr(), xs, positions.data_ptr(), T, heads, dim, rope._bytes, _ptr(gamma), eps, y.data_ptr(),
-            ys)
+        _expect(gamma, "gamma", _TWO, (dim,), index)
+    _launch_on(_lib.qlin_rope, index, stream, x.data_ptr(), xs, positions.data_ptr(), T, heads, dim, turn, _ptr(gamma), eps, y.data_ptr(), ys)
 
 
 _PACK_QUERIES = struct.Struct("QqQQqi4x").pack
@@ -785,42 +818,40 @@ def qlin_cache_write(cache, slots, k, v, positions=None, rope=None, q=None, q_ou
     """k, v bf16 [T, kv_heads, dim] (any stride between tokens) into slots int32 [T] of the cache (-1: not written), and
     q [T, heads, dim] into q_out (may be q), in one launch.  rope and positions int32 [T]: q and k are rotated;
     q_gamma, k_gamma bf16 [dim]: each head's RMS norm first."""
-    device, dim = cache.device, cache.dim
+    index, dim, kv_heads = cache._index, cache.dim, cache.kv_heads
     T = slots.shape[0] if slots.dim() == 1 else -1
-    _int32(slots, "slots", (T,), device)
-    ks, vs = _heads(k, "k", cache.kv_heads, dim, device, T), _heads(v, "v", cache.kv_heads, dim, device, T)
-    if (rope is None) != (positions is None):
+    _expect(slots, "slots", _INT32, (T,), index)
+    ks, vs = _heads(k, "k", T, kv_heads, dim, index), _heads(v, "v", T, kv_heads, dim, index)
+    turn = at = queries = None
+    if rope is not None and positions is not None:
+        turn, at = _rope_bytes(rope, positions, T, index), positions.data_ptr()
+    elif rope is not None or positions is not None:
         raise ValueError("rope and positions come together")
-    if rope is not None:
-        _int32(positions, "positions", (T,), device)
-        if rope.device != device:
-            raise ValueError(f"rope is on {rope.device}, the call runs on {device}")
     if k_gamma is not None:
-        _w4_tensor(k_gamma, "k_gamma", (dim,), 2, device)
-    queries = None
+        _expect(k_gamma, "k_gamma", _TWO, (dim,), index)
     if q is not None:
         if q.dim() != 3 or q_out is None or (rope is None and q_gamma is None):
             raise ValueError("q must be [T, heads, dim], with q_out, and rope or q_gamma")
         heads = q.shape[1]
-        qs, os = _heads(q, "q", heads, dim, device, T), _heads(q_out, "q_out", heads, dim, device, T)
+        qs, os = _heads(q, "q", T, heads, dim, index), _heads(q_out, "q_out", T, heads, dim, index)
         if q_gamma is not None:
-            _w4_tensor(q_gamma, "q_gamma", (dim,), 2, device)
-        queries = _PACK_QUERIES(q.data_ptr(), qs, _ptr(q_gamma) or 0, q_out.data_ptr(), os, heads)
+            _expect(q_gamma, "q_gamma", _TWO, (dim,), index)
+        queries = _PACK_QUERIES(q.data_ptr(), qs, 0 if q_gamma is None else q_gamma.data_ptr(), q_out.data_ptr(), os, heads)
     elif q_out is not None or q_gamma is not None:
         raise ValueError("q_out and q_gamma need q")
-    _launch(_lib.qlin_cache_write, device, stream, cache._bytes, slots.data_ptr(), T, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(positions),
-            None if rope is None else rope._bytes, _ptr(k_gamma), eps, queries)
+    _launch_on(_lib.qlin_cache_write, index, stream, cache._bytes, slots.data_ptr(), T, k.data_ptr(), ks, v.data_ptr(), vs, at, turn,
+               _ptr(k_gamma), eps, queries)
 
 
 def qlin_cache_read(cache, slots, k, v, stream=None):
     """k, v bf16 [n, kv_heads, dim] receive the keys and values of slots int32 [n]; rows of a slot outside the cache stay."""
-    device = cache.device
+    index = cache._index
     n = slots.shape[0] if slots.dim() == 1 else -1
-    _int32(slots, "slots", (n,), device)
+    _expect(slots, "slots", _INT32, (n,), index)
     shape = (n, cache.kv_heads, cache.dim)
-    _w4_tensor(k, "k", shape, 2, device)
-    _w4_tensor(v, "v", shape, 2, device)
-    _launch(_lib.qlin_cache_read, device, stream, cache._bytes, slots.data_ptr(), n, k.data_ptr(), v.data_ptr())
+    _expect(k, "k", _TWO, shape, index)
+    _expect(v, "v", _TWO, shape, index)
+    _launch_on(_lib.qlin_cache_read, index, stream, cache._bytes, slots.data_ptr(), n, k.data_ptr(), v.data_ptr())
 
 
 def qlin_attn_decode_workspace(heads, cache):
@@ -835,20 +866,21 @@ def qlin_attn_decode(q, cache, pages, lengths, out, workspace, scale=None, windo
     """Attention of one new token per sequence: q, out bf16 [S, heads, dim]; pages int32 [S, columns], the pages of each
     sequence's tokens; lengths int32 [S] (0: out is zero, negative: left as it was); window > 0: the last tokens alone;
     scale: dim ** -0.5 unless given; workspace uint8, qlin_attn_decode_workspace bytes."""
-    device, dim = cache.device, cache.dim
+    index, dim = cache._index, cache.dim
     if q.dim() != 3 or pages.dim() != 2:
         raise ValueError("q must be [S, heads, dim] and pages [S, columns]")
-    S, heads = q.shape[0], q.shape[1]
-    _w4_tensor(q, "q", (S, heads, dim), 2, device)
-    _w4_tensor(out, "out", (S, heads, dim), 2, device)
+    S, heads, _ = q.shape
+    shape = (S, heads, dim)
     columns = pages.shape[1]
-    _int32(pages, "pages", (S, columns), device)
-    _int32(lengths, "lengths", (S,), device)
-    _w4_tensor(workspace, "workspace", None, 1, device)
-    need = cache._workspaces.get(heads)
+    _expect(q, "q", _TWO, shape, index)
+    _expect(out, "out", _TWO, shape, index)
+    _expect(pages, "pages", _INT32, (S, columns), index)
+    _expect(lengths, "lengths", _INT32, (S,), index)
+    _expect(workspace, "workspace", _BYTE, None, index)
+    need = cache._workspaces.get(heads)    # (a size by the number of heads: it goes by the shapes alone)
     if need is None:
         need = cache._workspaces[heads] = _lib.qlin_attn_decode_workspace(heads, cache.kv_heads, dim)
     if workspace.numel() < need:
         raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
-    _launch(_lib.qlin_attn_decode, device, stream, q.data_ptr(), cache._bytes, pages.data_ptr(), S, heads, columns, lengths.data_ptr(), window,
-            dim ** -0.5 if scale is None else scale, out.data_ptr(), workspace.data_ptr())
+    _launch_on(_lib.qlin_attn_decode, index, stream, q.data_ptr(), cache._bytes, pages.data_ptr(), S, heads, columns, lengths.data_ptr(),
+               window, dim ** -0.5 if scale is None else scale, out.data_ptr(), workspace.data_ptr())

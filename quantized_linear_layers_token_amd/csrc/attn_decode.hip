@@ -16,12 +16,14 @@
 // in two bf16 parts (the matrix cores have the time: about a tenth of theirs
 // is used), which leaves 2^-17 of it.
 //
-// Work is cut in units of 32 tokens.  The units of all sequences, one after
-// the other, are shared evenly among `workers` workgroups per group of heads,
-// whatever the lengths: a workgroup finds its sequences by a scan of the
-// lengths.  A sequence within one workgroup is finished there; of one that
-// several share each writes a partial sum, and a second launch joins them.  So
-// the launches do not depend on the lengths and can be captured.
+// Work is cut in items (attn_index.h), one to a workgroup, so that they are
+// about even whatever the lengths: a workgroup finds its own by a scan of the
+// lengths.  A sequence of one item is finished by it; of one of several each
+// item writes a partial sum, and a second launch joins them.  So the launches do
+// not depend on the lengths and can be captured.  Where no sequence can be long,
+// or there are a great many, an item is a sequence and there is one launch.
+#include <type_traits>
+
 #include "attn_index.h"
 #include "layer_device.h"
 
@@ -43,12 +45,13 @@ struct AttnArgs {
     const float *k_scale, *v_scale;
     const int *pages, *lengths;
     uint16_t* out;
-    float* sums;      // partial sums [group of heads][worker][2][rows][dim]
-    float* stats;     // their maxima and sums of p [group of heads][worker][2][rows][2]
-    int* joins;       // [group of heads][worker][3]: sequence (-1: none), its last worker, the part of the first
+    float* sums;      // partial sums [group of heads][2 workers][rows][dim]: those of a split sequence follow each other
+    float* stats;     // their maxima and sums of p [group of heads][2 workers][rows][2]
+    int* joins;       // [group of heads]: 4 ints, the number of partial sums first, then for each {sequence, its first, their number, 0}
     int64_t npages;
     int S, heads, kv_heads, dim, columns, page_size, window;
     int tiles, rows, workers;
+    int items, least; // units are shared as for so many workgroups (at most workers), items are not cut below so many
     float scale;      // times log2 e
 };
 
@@ -88,6 +91,17 @@ __device__ __forceinline__ float column_sum(float v) {
 __device__ __forceinline__ uint32_t bits(v2bf v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ __forceinline__ v8bf operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return __builtin_bit_cast(v8bf, v4u{a, b, c, d}); }
 
+// Byte I of w, a signed integer, as f32 (one instruction; the compiler takes two or three).
+template <int I>
+__device__ __forceinline__ float signed_byte(uint32_t w) {
+    float f;
+    if constexpr (I == 0) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(w));
+    if constexpr (I == 1) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(w));
+    if constexpr (I == 2) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(w));
+    if constexpr (I == 3) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(w));
+    return f;
+}
+
 // Codes as bf16, exactly: a pair of bytes of w (E4M3: by one instruction;
 // int8: by way of f32, whose upper halves are the bf16 values).
 template <int KIND, bool HI>
@@ -95,7 +109,7 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
     if constexpr (KIND == QLIN_CACHE_FP8) {
         return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
     } else {
-        const float a = (float)(int8_t)(HI ? w >> 16 : w), b = (float)(int8_t)(HI ? w >> 24 : w >> 8);
+        const float a = signed_byte<HI ? 2 : 0>(w), b = signed_byte<HI ? 3 : 1>(w);
         return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
     }
 }
@@ -148,14 +162,18 @@ __device__ __forceinline__ unsigned scan(unsigned v) {
 }
 __device__ __forceinline__ unsigned lane_of(unsigned v, int lane) { return (unsigned)__builtin_amdgcn_readlane((int)v, lane); }
 
+// Wavefronts of a SIMD that the registers are bounded to.
+constexpr int waves_per_simd(int dp) { return dp == 64 ? 4 : dp == 128 ? 3 : 1; }
+
 // ALONE: a workgroup takes a whole sequence, and nothing is joined.
 template <int KIND, int DP, int WAVES, bool ALONE>
-__global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP)) void attn_kernel(AttnArgs a) {
     using T = Tiles<KIND, DP>;
     constexpr int kTiles = DP / 16, kSteps = DP / 32;
     constexpr int kPad = DP + 4;
-    __shared__ float joined[WAVES / 2][kAttnHeads * kPad];
-    __shared__ float stats[WAVES / 2][2][kAttnHeads];
+    constexpr int kSlots = WAVES / 2 < 4 ? WAVES / 2 : 4;
+    __shared__ float joined[kSlots][kAttnHeads * kPad];
+    __shared__ float stats[kSlots][2][kAttnHeads];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
     const int groups = a.kv_heads * a.tiles;
@@ -164,62 +182,66 @@ __global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(
     const int shared_by = a.heads / a.kv_heads;
     const int head0 = kv_head * shared_by + tile * kAttnHeads;
     const int rows = min(a.rows, shared_by - tile * kAttnHeads);
-    int* join = ALONE ? nullptr : a.joins + ((int64_t)group * a.workers + worker) * 3;
-
-    int s = 0;
-    int64_t before = 0, lo = 0, hi = 0, share = 0;   // units of the sequences before s; the workgroup's first and end; of each workgroup
+    AttnSpan span = {};
+    int s = 0, first = 0, last = 0, record = -1;   // the item: a sequence and its units; its partial sum (-1: the whole sequence)
     if constexpr (ALONE) {
         s = worker;
-        hi = span_of(table_of(a.lengths)[s], a).units;
+        span = span_of(table_of(a.lengths)[s], a);
+        last = (int)span.units;
     } else {
-        // the worker's units, and the sequence of the first of them
-        auto units_at = [&](int first) { return first + lane < a.S ? span_of(a.lengths[first + lane], a).units : 0; };
-        unsigned units = units_at(0), upto = scan(units);
-        int64_t total = lane_of(upto, kWave - 1);
-        for (int c = kWave; c < a.S; c += kWave) total += lane_of(scan(units_at(c)), kWave - 1);
-        share = attn_share(total, a.workers);
-        lo = worker * share, hi = lo < total ? min(lo + share, total) : 0;
-        if (threadIdx.x == 0) join[0] = -1;
-        if (lo < total) {
-            for (int c = 0;;) {
-                const uint64_t past = __ballot(before + upto > lo);
-                if (past) {
-                    const int at = __builtin_ctzll(past);
-                    s = c + at;
-                    before += lane_of(upto - units, at);
-                    break;
+        auto length_at = [&](int c) { return c + lane < a.S ? a.lengths[c + lane] : -1; };
+        AttnSpan of_lane = span_of(length_at(0), a);
+        int64_t total = lane_of(scan(of_lane.units), kWave - 1);
+        for (int c = kWave; c < a.S; c += kWave) total += lane_of(scan(span_of(length_at(c), a).units), kWave - 1);
+        const unsigned most = attn_most(total, a.items, a.least);
+        unsigned items = 0, split = 0;   // of the sequences before a chunk of 64: items, and those of split sequences
+        bool found = false;
+        for (int c = 0; c < a.S; c += kWave) {
+            if (c) of_lane = span_of(length_at(c), a);
+            const unsigned n = attn_items(of_lane.units, most), upto = scan(n), split_upto = scan(n > 1 ? n : 0);
+            const uint64_t past = __ballot(items + upto > (unsigned)worker);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                const unsigned of = lane_of(n, at), i = worker - (items + lane_of(upto, at) - of);
+                s = c + at;
+                span = AttnSpan{(int)lane_of(of_lane.n, at), (int)lane_of(of_lane.start, at), lane_of(of_lane.units, at)};
+                first = (int)attn_first_unit(span.units, of, i), last = (int)attn_first_unit(span.units, of, i + 1);
+                if (of > 1) {
+                    const int begin = (int)(split + lane_of(split_upto, at) - of);
+                    record = begin + (int)i;
+                    if (threadIdx.x == 0)
+                        *reinterpret_cast<v4i*>(a.joins + 4 * ((int64_t)group * (2 * a.workers + 1) + 1 + record)) = v4i{s, begin, (int)of, 0};
                 }
-                before += lane_of(upto, kWave - 1);
-                c += kWave;
-                units = units_at(c), upto = scan(units);
+                found = true;
+                break;
             }
+            items += lane_of(upto, kWave - 1), split += lane_of(split_upto, kWave - 1);
         }
+        // the first workgroup without an item has seen them all
+        if (!found && items == (unsigned)worker && threadIdx.x == 0) a.joins[4 * (int64_t)group * (2 * a.workers + 1)] = (int)split;
     }
 
     const int64_t row_bytes = (int64_t)a.dim * T::kBytes;
-    // byte offsets in a row: the lane's quarter of the channels as 16-byte chunks (keys), its DP / 16 channels (values)
+    // byte offsets in a row: the lane's 16-byte chunks (keys: every fourth, so that four lanes read 64 bytes at once),
+    // its DP / 16 channels (values)
     int key_at[T::kKeyChunks];
 #pragma unroll
     for (int i = 0; i < T::kKeyChunks; ++i) {
-        const int at = g * (DP / 4 * T::kBytes) + 16 * i;
+        const int at = 16 * (4 * i + g);
         key_at[i] = n * (int)row_bytes + (at < row_bytes ? at : 0);
     }
     const int value_piece = n * (DP / 16 * T::kBytes);
     const int value_at = 4 * g * (int)row_bytes + (value_piece < row_bytes ? value_piece : 0);
 
-    for (; before < hi; ++s) {   // (hi is at most the units of all: the loop ends before s leaves the batch)
-        s = __builtin_amdgcn_readfirstlane(s);
-        const AttnSpan span = span_of(table_of(a.lengths)[s], a);
-        if (span.units == 0) continue;
-        const int first = (int)(max(lo, before) - before), last = (int)(min(hi, before + span.units) - before);
-        // the wavefront's units of them
-        const int mine = first + (int)((int64_t)(last - first) * wave / WAVES);
-        const int end = first + (int)((int64_t)(last - first) * (wave + 1) / WAVES);
+    if (first < last) {
+        // the wavefront's units of the item
+        const int mine = first + (last - first) * wave / WAVES, end = first + (last - first) * (wave + 1) / WAVES;
 
         v8bf q[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int d = g * (DP / 4) + 8 * i;
+            // the channels of the key chunks: 8 to a chunk in bf16, 16 (two operands) in 8 bits
+            const int d = KIND == QLIN_CACHE_BF16 ? 8 * (4 * i + g) : 16 * (4 * (i / 2) + g) + 8 * (i % 2);
             v4u w = v4u{0, 0, 0, 0};
             if (n < rows && d < a.dim) w = *reinterpret_cast<const v4u*>(a.q + ((int64_t)s * a.heads + head0 + n) * a.dim + d);
             q[i] = __builtin_bit_cast(v8bf, w);
@@ -260,8 +282,8 @@ __global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(
 #pragma unroll
         for (int r = 0; r < kTiles; ++r) acc[r] = v4f{0, 0, 0, 0};
 
-        T t;
-        Places here, next;
+        T t = {};
+        Places here = {}, next = {};
         if (mine < end) {
             here = where(mine);
             load_keys(here, t);
@@ -323,6 +345,13 @@ __global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(
                         if constexpr (KIND != QLIN_CACHE_BF16) t.value_scale[j][i] = live ? t.value_scale[j][i] : 0.0f;
                     }
                 }
+            }
+            // Single registers from here on: this compiler has lost the upper half of loaded pairs that were still to be
+            // used (the register allocator gave them to p), here and in no other form that was read or tested.
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                for (int w = 0; w < T::kValueDwords; ++w) asm("" : "+v"(t.value[i][w]));
             }
             v8bf high, low;
 #pragma unroll
@@ -406,16 +435,18 @@ __global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(
         };
 #pragma unroll
         for (int half = WAVES / 2; half >= 1; half /= 2) {
-            __syncthreads();   // the buffers are free
-            if (wave >= half && wave < 2 * half) give(wave - half);
-            __syncthreads();
-            if (wave < half) take(wave);
+#pragma unroll
+            for (int w = 0; w < half; w += kSlots) {   // wavefronts w .. of the lower half take from those of the upper
+                __syncthreads();   // the buffers are free
+                if (wave >= half + w && wave < half + min(w + kSlots, half)) give(wave - half - w);
+                __syncthreads();
+                if (wave >= w && wave < min(w + kSlots, half)) take(wave - w);
+            }
         }
 
-        const bool starts = before >= lo, ends = before + span.units <= hi;
         if (wave == 0 && n < rows) {
             const int d0 = 4 * g * kTiles;
-            if (ALONE || (starts && ends)) {
+            if (ALONE || record < 0) {
                 const float by = l > 0.0f || l != l ? 1.0f / l : 0.0f;
                 uint16_t* to = a.out + ((int64_t)s * a.heads + head0 + n) * a.dim + d0;
 #pragma unroll
@@ -426,8 +457,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(
                             *reinterpret_cast<uint32_t*>(to + i * kTiles + r) = bf16_pair(acc[r][i] * by, acc[r + 1][i] * by);
                 }
             } else {
-                const int part = attn_part(before, lo);
-                const int64_t at = (((int64_t)group * a.workers + worker) * 2 + part) * a.rows + n;
+                const int64_t at = ((int64_t)group * 2 * a.workers + record) * a.rows + n;
                 float* to = a.sums + at * a.dim + d0;
                 if (g == 0) *reinterpret_cast<v2f*>(a.stats + 2 * at) = v2f{m, l};
 #pragma unroll
@@ -437,89 +467,107 @@ __global__ __launch_bounds__(WAVES * kWave, DP == 256 ? 1 : 2) void attn_kernel(
                         if (d0 + i * kTiles + r < a.dim)
                             *reinterpret_cast<v4f*>(to + i * kTiles + r) = v4f{acc[r][i], acc[r + 1][i], acc[r + 2][i], acc[r + 3][i]};
                 }
-                if (starts && lane == 0) {
-                    join[0] = s;
-                    join[1] = attn_last_worker(before, span.units, share);
-                    join[2] = part;
-                }
             }
         }
-        before += span.units;
     }
 
-    // sequences without tokens: zeros, a share of them for each workgroup
-    for (int e = worker * WAVES + wave; e < (ALONE ? (wave == 0 ? worker * WAVES + 1 : 0) : a.S); e += a.workers * WAVES) {
-        const int of = ALONE ? worker : e, length = table_of(a.lengths)[of];
+    // sequences without tokens: zeros
+    auto clear = [&](int e) {
+        const int length = table_of(a.lengths)[e];
         if (length == 0 || (length > 0 && a.columns == 0))
             for (int i = lane; i < rows * a.dim / 2; i += kWave)
-                reinterpret_cast<uint32_t*>(a.out + ((int64_t)of * a.heads + head0) * a.dim)[i] = 0;
+                reinterpret_cast<uint32_t*>(a.out + ((int64_t)e * a.heads + head0) * a.dim)[i] = 0;
+    };
+    if constexpr (ALONE) {
+        if (wave == 0) clear(s);
+    } else {   // a share of them for each workgroup
+        for (int e = worker * WAVES + wave; e < a.S; e += (a.workers + a.S + 1) * WAVES) clear(e);
     }
 }
 
-// A workgroup joins the parts of the sequence that began with a worker and went
-// on, a wavefront one query head at a time: lane p holds the maximum and the
-// sum of part p, the values of eight parts are under way together.
+// Joins the partial sums of split sequences.  The workgroup of partial sum r
+// takes the query heads r - begin, r - begin + n, .. of its sequence, whose n
+// partial sums begin at `begin`; the wavefronts take every fourth of them, lane
+// p the maximum and sum of the p-th of these, and the values of 16 are under way
+// together.
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
-    constexpr int kTogether = 8;
+    __shared__ float part_max[kWaves], part_sum[kWaves];
+    __shared__ float part_out[kWaves][QLIN_MAX_HEAD_DIM];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int groups = a.kv_heads * a.tiles;
-    const int group = blockIdx.x % groups, worker = blockIdx.x / groups;
-    const Table join = table_of(a.joins + ((int64_t)group * a.workers + worker) * 3);
-    const int s = join[0], last = join[1], part = join[2];
-    if (s < 0) return;
+    const int group = blockIdx.x % groups, record = blockIdx.x / groups;
+    const Table joins = table_of(a.joins + 4 * ((int64_t)group * (2 * a.workers + 1)));
+    const int records = joins[0], s = joins[4 * (1 + record)], begin = joins[4 * (1 + record) + 1], parts = joins[4 * (1 + record) + 2];
+    if (record >= records) return;
     const int shared_by = a.heads / a.kv_heads, tile = group % a.tiles;
     const int rows = min(a.rows, shared_by - tile * kAttnHeads);
-    const int parts = last - worker + 1;
-    auto record = [&](int p, int row) {   // part p: the first lies in `part`, the others over their worker's first unit
-        return (((int64_t)group * a.workers + worker + p) * 2 + (p == 0 ? part : 0)) * a.rows + row;
-    };
-    for (int row = wave; row < rows; row += kWaves) {
+    const int mine = (parts - wave + kWaves - 1) / kWaves;   // the wavefront's partial sums: wave, wave + 4, ..
+    for (int row = record - begin; row < rows; row += parts) {
+        auto at = [&](int p) { return ((int64_t)group * 2 * a.workers + begin + wave + kWaves * p) * a.rows + row; };
         float m = kNone, l = 0.0f, o[4] = {0, 0, 0, 0};
-        for (int p0 = 0; p0 < parts; p0 += kWave) {
-            v2f mine = v2f{kNone, 0.0f};
-            if (p0 + lane < parts) mine = *reinterpret_cast<const v2f*>(a.stats + 2 * record(p0 + lane, row));
-            const int here = min(parts - p0, kWave);
-            float top = lanes_max<16>(mine.x);
-            top = fmaxf(m, column_max(top));
-            const float zero_at = top == kNone ? 0.0f : top;
-            const float weight = __builtin_amdgcn_exp2f(mine.x - zero_at), by = __builtin_amdgcn_exp2f(m - zero_at);
-            l = l * by + column_sum(lanes_sum<16>(mine.y * weight));
-            m = top;
+        for (int p0 = 0; p0 < mine; p0 += kWave) {
+            const int here = min(mine - p0, kWave);
+            v2f stat = v2f{kNone, 0.0f};
+            if (lane < here) stat = *reinterpret_cast<const v2f*>(a.stats + 2 * at(p0 + lane));
+            float weight = 0.0f;
+            auto batch = [&](auto count, int p) {   // the values of partial sums p .. p + count - 1, under way together
+                constexpr int kCount = decltype(count)::value;
+                v2f x[kCount][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= by;
-            for (int p = 0; p < here; p += kTogether) {
-                v2f x[kTogether][2];
-#pragma unroll
-                for (int u = 0; u < kTogether; ++u) {
-                    const float* from = a.sums + record(p0 + min(p + u, here - 1), row) * a.dim;
+                for (int u = 0; u < kCount; ++u) {
+                    const float* from = a.sums + at(p0 + min(p + u, here - 1)) * a.dim;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int d = 2 * lane + 128 * i;
                         x[u][i] = d < a.dim ? *reinterpret_cast<const v2f*>(from + d) : v2f{0, 0};
                     }
                 }
+                if (p == 0) {
+                    const float top = fmaxf(m, column_max(lanes_max<16>(stat.x))), zero_at = top == kNone ? 0.0f : top;
+                    const float by = __builtin_amdgcn_exp2f(m - zero_at);
+                    weight = __builtin_amdgcn_exp2f(stat.x - zero_at);
+                    l = l * by + column_sum(lanes_sum<16>(stat.y * weight));
+                    m = top;
 #pragma unroll
-                for (int u = 0; u < kTogether; ++u) {
+                    for (int i = 0; i < 4; ++i) o[i] *= by;
+                }
+#pragma unroll
+                for (int u = 0; u < kCount; ++u) {
                     const float w = p + u < here ? __uint_as_float(lane_of(__float_as_uint(weight), min(p + u, kWave - 1))) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[u][i / 2][i % 2], w, o[i]);
                 }
-            }
+            };
+            int p = 0;
+            for (; here - p > 4; p += 16) batch(std::integral_constant<int, 16>{}, p);
+            if (p < here) batch(std::integral_constant<int, 4>{}, p);
         }
-        const float by = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        const int head = group / a.tiles * shared_by + tile * kAttnHeads + row;
-        uint16_t* to = a.out + ((int64_t)s * a.heads + head) * a.dim;
+        __syncthreads();   // the buffers are free
+        if (lane == 0) part_max[wave] = m, part_sum[wave] = l;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int d = 2 * lane + 128 * i;
-            if (d < a.dim) *reinterpret_cast<uint32_t*>(to + d) = bf16_pair(o[2 * i] * by, o[2 * i + 1] * by);
+        for (int i = 0; i < 4; ++i) part_out[wave][2 * lane + 128 * (i / 2) + i % 2] = o[i];
+        __syncthreads();
+        const int d = threadIdx.x;
+        if (d < a.dim) {
+            float top = kNone, sum = 0.0f, out = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, part_max[w]);
+            top = top == kNone ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float by = __builtin_amdgcn_exp2f(part_max[w] - top);
+                sum += part_sum[w] * by;
+                out += part_out[w][d] * by;
+            }
+            const int head = group / a.tiles * shared_by + tile * kAttnHeads + row;
+            a.out[((int64_t)s * a.heads + head) * a.dim + d] = f32_to_bf16(sum > 0.0f || sum != sum ? out / sum : 0.0f);
         }
     }
 }
 
 template <int KIND, int DP>
 void launch_dim(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
-    constexpr int kAlone = DP == 256 ? kWaves : 8;   // (heads of 256 channels take the registers of a SIMD for one wavefront)
+    constexpr int kAlone = DP == 64 ? 8 : kWaves;
     if (alone) hipLaunchKernelGGL((attn_kernel<KIND, DP, kAlone, true>), dim3(grid), dim3(kAlone * kWave), 0, st, a);
     else hipLaunchKernelGGL((attn_kernel<KIND, DP, kWaves, false>), dim3(grid), dim3(kThreads), 0, st, a);
 }
@@ -530,25 +578,27 @@ void launch_kind(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
     else launch_dim<KIND, 256>(a, alone, grid, st);
 }
 
-// Tables of up to this many tokens a sequence take a workgroup for each sequence
-// and one launch.
-constexpr int64_t kAloneTokens = 2048;
+// An item is a sequence, and there is one launch, where no sequence can be
+// longer than two steps of a workgroup's wavefronts, or than kMedium and their
+// number fills half of the CUs; and for more sequences than a workgroup can scan.
+constexpr int64_t kMedium = 2048;
+constexpr int kScanned = 1024;
 constexpr int64_t kMaxGrid = int64_t(1) << 22;   // workgroups of 512 threads: a launch holds 2^32 threads
-constexpr int kResident = 512;   // workgroups of four wavefronts that the card holds at once: two on each CU
+constexpr int kCus = 256;
 
 }  // namespace
 
 AttnShape attn_shape(int heads, int kv_heads, int dim) {
-    (void)dim;
+    const int resident = kCus * waves_per_simd(dim <= 64 ? 64 : dim <= 128 ? 128 : 256);
     const int shared_by = heads / kv_heads, tiles = (shared_by + kAttnHeads - 1) / kAttnHeads;
     const int groups = kv_heads * tiles;
-    return AttnShape{tiles, shared_by < kAttnHeads ? shared_by : kAttnHeads, groups >= kResident ? 1 : kResident / groups};
+    return AttnShape{tiles, shared_by < kAttnHeads ? shared_by : kAttnHeads, groups >= resident ? 1 : resident / groups};
 }
 
 int64_t attn_workspace(int heads, int kv_heads, int dim) {
     const AttnShape s = attn_shape(heads, kv_heads, dim);
-    const int64_t records = (int64_t)kv_heads * s.tiles * s.workers;
-    return records * 2 * s.rows * (dim + 2) * 4 + (records * 3 * 4 + 15) / 16 * 16;
+    const int64_t groups = (int64_t)kv_heads * s.tiles, records = groups * 2 * s.workers;
+    return 16 * (groups + records) + records * s.rows * (dim + 2) * 4;
 }
 
 hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
@@ -563,10 +613,10 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.pages = c.pages;
     a.lengths = c.lengths;
     a.out = c.out;
-    a.sums = static_cast<float*>(c.workspace);
-    const int64_t records = (int64_t)groups * shape.workers * 2 * shape.rows;
-    a.stats = a.sums + records * c.cache.dim;
-    a.joins = reinterpret_cast<int*>(a.stats + records * 2);
+    const int64_t records = (int64_t)groups * 2 * shape.workers;
+    a.joins = static_cast<int*>(c.workspace);
+    a.stats = reinterpret_cast<float*>(a.joins + 4 * (groups + records));
+    a.sums = a.stats + records * shape.rows * 2;
     a.npages = c.cache.pages;
     a.S = c.S;
     a.heads = c.heads;
@@ -578,16 +628,35 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.tiles = shape.tiles;
     a.rows = shape.rows;
     a.workers = shape.workers;
+    // There are up to workers + S items: one round of workgroups where the sequences are few beside them.  Where they are
+    // many, a sequence of 512 tokens is not cut (64 of 256 tokens, 32 / 8 heads of 128: 18.2 us cut in two, 13.4 whole).
+    const bool few = c.S <= shape.workers / 2;
+    a.items = few ? shape.workers - c.S : shape.workers;
+    a.least = few ? kAttnWaves : 4 * kAttnWaves;
     a.scale = c.scale * 1.44269504088896340736f;
-    // (64-bit: S times the groups of heads)
-    const bool alone = (int64_t)c.columns * c.cache.page_size <= kAloneTokens && (int64_t)c.S * groups <= kMaxGrid;
-    const unsigned grid = (unsigned)(alone ? (int64_t)c.S * groups : (int64_t)groups * shape.workers);
+    const int64_t tokens = (int64_t)c.columns * c.cache.page_size, whole = (int64_t)c.S * groups;
+    const bool alone = tokens <= (c.cache.dim <= 64 ? 512 : 256) || (tokens <= kMedium && whole >= kCus / 2) || c.S > kScanned;
+    const int64_t most = alone ? whole : (int64_t)groups * (shape.workers + c.S + 1);
+    if (most > kMaxGrid) {   // one half of the sequences after the other
+        AttnCall part = c;
+        part.S = c.S / 2;
+        const hipError_t e = launch_attn(part, st);
+        if (e != hipSuccess) return e;
+        const int64_t done = part.S;
+        part.S = c.S - part.S;
+        part.q += done * c.heads * c.cache.dim;
+        part.out += done * c.heads * c.cache.dim;
+        if (c.columns) part.pages += done * c.columns;
+        part.lengths += done;
+        return launch_attn(part, st);
+    }
+    const unsigned grid = (unsigned)most;
     if (c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(a, alone, grid, st);
     else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(a, alone, grid, st);
     else launch_kind<QLIN_CACHE_FP8>(a, alone, grid, st);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && !alone && shape.workers > 1) {
-        hipLaunchKernelGGL(attn_join_kernel, dim3(grid), dim3(kThreads), 0, st, a);
+    if (e == hipSuccess && !alone) {
+        hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(groups * 2 * shape.workers)), dim3(kThreads), 0, st, a);
         e = hipGetLastError();
     }
     return e;

@@ -1,6 +1,14 @@
 // Which tokens a workgroup of the attention takes and where they lie: the
 // integer part of attn_decode.hip, in functions that host code can run too
 // (constexpr: for either side), so that every bound is tested on the CPU.
+//
+// A sequence's tokens are cut in units of 32, and the units in items, one to a
+// workgroup: a sequence of up to `most` units is one item, a longer one
+// ceil(units / most) of about equal size.  With most = ceil(total / workers)
+// or more there are at most workers + S items,
+// whatever the lengths, and at most 2 workers of them belong to sequences of
+// several (whose partial sums are written down and joined): n > 1 means
+// units > most, so n < 2 units / most.
 #pragma once
 
 #include <stdint.h>
@@ -26,19 +34,18 @@ constexpr AttnSpan attn_span(int length, int columns, int page_size, int window)
     return AttnSpan{n, start, (unsigned)((n + kAttnUnit - 1) / kAttnUnit - start / kAttnUnit)};
 }
 
-// Units of one workgroup: an even share, but one for each wavefront at least.
-constexpr int64_t attn_share(int64_t total, int workers) {
+// Units of an item at most; `least` (kAttnWaves or more) where the shares are smaller.
+constexpr unsigned attn_most(int64_t total, int workers, int least) {
     const int64_t even = (total + workers - 1) / workers;
-    return even > kAttnWaves ? even : kAttnWaves;
+    return even < least ? (unsigned)least : even > 0x7fffffff ? 0x7fffffffu : (unsigned)even;
 }
-
-// The part of a workgroup's partial sums that a sequence takes whose first unit
-// is `before` and that the workgroup, whose first unit is `lo`, does not hold
-// whole: 0 for the one that lies over the workgroup's first unit, 1 for one
-// that begins later (and goes on past its last).
-constexpr int attn_part(int64_t before, int64_t lo) { return before > lo ? 1 : 0; }
-// The workgroup that holds a sequence's last unit.
-constexpr int attn_last_worker(int64_t before, unsigned units, int64_t share) { return (int)((before + units - 1) / share); }
+// Items of a sequence.
+constexpr unsigned attn_items(unsigned units, unsigned most) { return (units + most - 1) / most; }
+// Of these, the first unit of item i of n (the end of the last: i = n).
+constexpr unsigned attn_first_unit(unsigned units, unsigned n, unsigned i) {
+    const unsigned each = units / n, more = units - each * n;
+    return i * each + (i < more ? i : more);
+}
 
 // One half of a unit: the row of the cache (page, kv head, place) of its first
 // token and which of its 16 tokens are live, lo <= i < hi.  A half without any

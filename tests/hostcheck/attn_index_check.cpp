@@ -1,11 +1,10 @@
 // The attention's integer part (attn_index.h) on the CPU: over random batches, every live token is taken exactly once,
-// every row that is loaded lies in the cache, every table entry that is read lies in the table, and the partial sums that
-// are written are those that are joined.
+// every row that is loaded lies in the cache, every table entry that is read lies in the table, and there is a
+// workgroup for every item and room for every partial sum.
 #include <cstdio>
 #include <cstdlib>
-#include <map>
+#include <initializer_list>
 #include <random>
-#include <set>
 #include <vector>
 
 #include "../../quantized_linear_layers_token_amd/csrc/attn_index.h"
@@ -38,35 +37,31 @@ int main() {
         for (int& v : length) v = draw(0, 5) == 0 ? draw(-2, 1) : draw(0, columns * page_size + 20);
         for (int& v : table) v = draw(0, 30) == 0 ? draw(-3, pages + 3) : draw(0, pages - 1);
         std::vector<AttnSpan> span(S);
-        std::vector<int64_t> before(S);
         int64_t total = 0;
         for (int s = 0; s < S; ++s) {
             span[s] = attn_span(length[s], columns, page_size, window);
-            before[s] = total;
             total += span[s].units;
             CHECK((span[s].units == 0) == (length[s] <= 0 || columns == 0));
         }
-        const int64_t share = attn_share(total, workers);
-        CHECK(share * workers >= total);
-        std::map<std::pair<int, int>, std::set<std::pair<int, int>>> parts;   // (worker, part) -> sequences that write it
-        std::map<int, std::set<std::pair<int, int>>> of_sequence;             // sequence -> its parts
-        std::map<int, std::vector<int>> join;                                 // worker -> sequence, last, part
+        const unsigned most = attn_most(total, workers, kAttnWaves * draw(1, 4));
+        unsigned items = 0, split = 0;
         std::vector<std::vector<int>> taken(S);
-        for (int s = 0; s < S; ++s) taken[s].assign((size_t)span[s].n, 0);
-        for (int w = 0; w < workers; ++w) {
-            const int64_t lo = w * share, hi = lo + share < total ? lo + share : total;
-            if (lo >= total) continue;
-            for (int s = 0; s < S; ++s) {
-                if (span[s].units == 0 || before[s] >= hi || before[s] + span[s].units <= lo) continue;
-                const int first = (int)((lo > before[s] ? lo : before[s]) - before[s]);
-                const int64_t stop = before[s] + span[s].units;
-                const int last = (int)((hi < stop ? hi : stop) - before[s]);
-                int reached = first;
+        for (int s = 0; s < S; ++s) {
+            taken[s].assign((size_t)span[s].n, 0);
+            const unsigned n = attn_items(span[s].units, most);
+            CHECK((n == 0) == (span[s].units == 0));
+            items += n;
+            split += n > 1 ? n : 0;
+            unsigned reached = 0;
+            for (unsigned i = 0; i < n; ++i) {
+                const unsigned first = attn_first_unit(span[s].units, n, i), last = attn_first_unit(span[s].units, n, i + 1);
+                CHECK(first == reached && last > first && last - first <= most);
+                reached = last;
+                int wave_reached = (int)first;
                 for (int wave = 0; wave < kAttnWaves; ++wave) {
-                    const int mine = first + (int)((int64_t)(last - first) * wave / kAttnWaves);
-                    const int end = first + (int)((int64_t)(last - first) * (wave + 1) / kAttnWaves);
-                    CHECK(mine == reached);
-                    reached = end;
+                    const int mine = first + (int)(last - first) * wave / kAttnWaves, end = first + (int)(last - first) * (wave + 1) / kAttnWaves;
+                    CHECK(mine == wave_reached);
+                    wave_reached = end;
                     for (int u = mine; u < end; ++u) {
                         ++units_seen;
                         for (int half = 0; half < 2; ++half) {
@@ -86,29 +81,13 @@ int main() {
                         }
                     }
                 }
-                CHECK(reached == last);
-                const bool starts = before[s] >= lo, ends = stop <= hi;
-                if (starts && ends) continue;
-                const int part = attn_part(before[s], lo);
-                parts[{w, part}].insert({s, w});
-                of_sequence[s].insert({w, part});
-                if (starts) {
-                    CHECK(!join.count(w));
-                    join[w] = {s, attn_last_worker(before[s], span[s].units, share), part};
-                }
+                CHECK(wave_reached == (int)last);
             }
+            CHECK(reached == span[s].units);
+            joined_seen += n > 1;
         }
-        for (const auto& p : parts) CHECK(p.second.size() == 1);
-        std::set<int> begun;
-        for (const auto& j : join) {
-            std::set<std::pair<int, int>> read;
-            for (int w = j.first; w <= j.second[1]; ++w) read.insert({w, w == j.first ? j.second[2] : 0});
-            CHECK(read == of_sequence[j.second[0]]);
-            CHECK(j.second[1] < workers);
-            begun.insert(j.second[0]);
-            ++joined_seen;
-        }
-        CHECK(begun.size() == of_sequence.size());
+        CHECK(items <= (unsigned)(workers + S));     // a workgroup for each, and one more that has none
+        CHECK(split <= (unsigned)(2 * workers));     // room for each partial sum
         for (int s = 0; s < S; ++s) {
             for (int t = 0; t < span[s].n; ++t) {
                 const int page = table[(size_t)s * columns + t / page_size];
@@ -122,8 +101,13 @@ int main() {
     CHECK(most.n == 1 << 30 && most.units == 1u << 25);
     const AttnSpan windowed = attn_span(0x7fffffff, 1 << 26, 16, 1);
     CHECK(windowed.units == 1 && windowed.start == (1 << 30) - 1);
-    const int64_t total = (int64_t)(1 << 24) << 25;
-    CHECK(attn_last_worker(total - (1 << 25), 1u << 25, attn_share(total, 512)) == 511);
+    for (int workers : {1, 2, 96, 1024})
+        for (int64_t total : {(int64_t)1 << 25, (int64_t)1 << 30, (int64_t)1024 << 25}) {
+            const unsigned m = attn_most(total, workers, kAttnWaves), units = 1u << 25, n = attn_items(units, m);
+            CHECK(n >= 1 && (int64_t)n * (total >> 25) <= 2 * (int64_t)workers + (total >> 25));
+            CHECK(attn_first_unit(units, n, 0) == 0 && attn_first_unit(units, n, n) == units);
+            for (unsigned i = 0; i < n; ++i) CHECK(attn_first_unit(units, n, i) < attn_first_unit(units, n, i + 1));
+        }
     std::printf("%ld units, %ld joins, %ld tokens: every bound held\n", units_seen, joined_seen, live_seen);
     return 0;
 }

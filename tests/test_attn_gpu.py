@@ -99,17 +99,36 @@ def test_lengths_at_the_edges(kind, page):
 @pytest.mark.parametrize("heads,kv_heads,dim", [(1, 1, 16), (2, 2, 32), (3, 1, 64), (20, 4, 64), (8, 8, 80), (5, 1, 96), (16, 1, 128), (17, 1, 128),
                                                 (40, 1, 64), (33, 3, 48), (32, 8, 128), (4, 2, 144), (6, 2, 192), (8, 1, 256), (34, 2, 256),
                                                 (7, 7, 112)])
-def test_head_layouts(kind, heads, kv_heads, dim):
-    c = Case(2, kind, [130, 7, 0, 33, 64], heads, kv_heads, dim, 32).load()
+@pytest.mark.parametrize("columns", [None, 300])    # one launch, or items that are joined
+def test_head_layouts(kind, heads, kv_heads, dim, columns):
+    c = Case(2, kind, [130, 7, 0, 33, 64, 290], heads, kv_heads, dim, 32, columns=columns).load()
     c.check(c.run())
+    c.check(c.run(window=50), window=50)
 
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("lengths", [[1], [777], [5000], [9000, 3, 0, 0, 12, 2500], [100] * 70, [0] * 65 + [300] + [0] * 70 + [40], [0], [-1, -7],
                                      [0, 0, 0]])
-def test_split_and_joined(kind, lengths):
-    c = Case(3, kind, lengths, 4, 2, 64, 16).load()
+@pytest.mark.parametrize("columns", [None, 700])
+def test_split_and_joined(kind, lengths, columns):
+    c = Case(3, kind, lengths, 4, 2, 64, 16, columns=columns).load()
     c.check(c.run())
+
+
+@pytest.mark.parametrize("S", [1023, 1024, 1025, 3000])
+def test_many_sequences(S):
+    rng = np.random.default_rng(S)
+    lengths = rng.integers(-1, 20, S)
+    lengths[[0, S // 2, S - 1]] = [700, 1300, 333]
+    c = Case(14, "int8", lengths.tolist(), 2, 1, 32, 16, columns=200).load()
+    c.check(c.run())
+
+
+def test_one_group_of_heads_and_many_parts():
+    """A single kv head: up to a thousand partial sums of one sequence, the join's loops over 64 and over 16 of them."""
+    for dim, n in ((64, 70000), (128, 9000), (256, 40000)):
+        c = Case(15, "fp8", [n, 100, 0], 17, 1, dim, 64).load()
+        c.check(c.run())
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -77,7 +77,7 @@ def test_validation_layer_under_sanitizers(tmp_path):
 
 def test_attention_indices_in_host_code(tmp_path):
     """Bad pages, windows, ragged and empty sequences: every row that would be loaded lies in the cache, every live token
-    is taken once, and the partial sums joined are those written."""
+    is taken once, and there is a workgroup for every item and room for every partial sum."""
     if shutil.which("g++") is None:
         pytest.skip("g++ is not installed")
     exe = str(tmp_path / "attn_index_check")
