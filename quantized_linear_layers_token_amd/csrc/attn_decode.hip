@@ -37,6 +37,7 @@ typedef unsigned v8u __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = kAttnWaves;
 constexpr int kThreads = kWaves * kWave;
+constexpr int kTries = 4;                     // for a size of items that fits the card
 constexpr float kNone = -__builtin_inff();    // score of no token
 
 struct AttnArgs {
@@ -51,7 +52,7 @@ struct AttnArgs {
     int64_t npages;
     int S, heads, kv_heads, dim, columns, page_size, window;
     int tiles, rows, workers;
-    int items, least; // units are shared as for so many workgroups (at most workers), items are not cut below so many
+    int least;        // items are not cut below so many units
     float scale;      // times log2 e
 };
 
@@ -162,12 +163,14 @@ __device__ __forceinline__ unsigned scan(unsigned v) {
 }
 __device__ __forceinline__ unsigned lane_of(unsigned v, int lane) { return (unsigned)__builtin_amdgcn_readlane((int)v, lane); }
 
-// Wavefronts of a SIMD that the registers are bounded to.
-constexpr int waves_per_simd(int dp) { return dp == 64 ? 4 : dp == 128 ? 3 : 1; }
+// Wavefronts of a SIMD that the registers are bounded to.  Heads of 256
+// channels in 8 bits: 53 us with two (a few registers spilled), 77 with one, for
+// 16 x 4096 tokens of 16 / 8 heads; in bf16 122 and 119.
+constexpr int waves_per_simd(int dp, bool bf16) { return dp == 64 ? 4 : dp == 128 ? 3 : bf16 ? 1 : 2; }
 
 // ALONE: a workgroup takes a whole sequence, and nothing is joined.
 template <int KIND, int DP, int WAVES, bool ALONE>
-__global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP)) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP, KIND == QLIN_CACHE_BF16)) void attn_kernel(AttnArgs a) {
     using T = Tiles<KIND, DP>;
     constexpr int kTiles = DP / 16, kSteps = DP / 32;
     constexpr int kPad = DP + 4;
@@ -193,7 +196,14 @@ __global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP)) void attn_kernel
         AttnSpan of_lane = span_of(length_at(0), a);
         int64_t total = lane_of(scan(of_lane.units), kWave - 1);
         for (int c = kWave; c < a.S; c += kWave) total += lane_of(scan(span_of(length_at(c), a).units), kWave - 1);
-        const unsigned most = attn_most(total, a.items, a.least);
+        unsigned most = attn_most(total, a.workers, a.least);
+        if (a.S <= kWave && a.S < a.workers) {   // as many items as workers at most: even on the CUs
+            for (int k = 0; k < kTries; ++k) {
+                const unsigned n = lane_of(scan(attn_items(of_lane.units, most)), kWave - 1);
+                if (n <= (unsigned)a.workers) break;
+                most = attn_larger(most, n, a.workers);
+            }
+        }
         unsigned items = 0, split = 0;   // of the sequences before a chunk of 64: items, and those of split sequences
         bool found = false;
         for (int c = 0; c < a.S; c += kWave) {
@@ -485,12 +495,65 @@ __global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP)) void attn_kernel
     }
 }
 
-// Joins the partial sums of split sequences.  The workgroup of partial sum r
-// takes the query heads r - begin, r - begin + n, .. of its sequence, whose n
-// partial sums begin at `begin`; the wavefronts take every fourth of them, lane
-// p the maximum and sum of the p-th of these, and the values of 16 are under way
-// together.
+// A head's running maximum, sum of p and (unnormalised) output: lane l of the
+// wavefront holds channels 2 l, 2 l + 1, 128 + 2 l and 129 + 2 l.
+struct Joined {
+    float m, l, o[4];
+};
+
+// The partial sums first, first + step, .. (count of them) of one query head:
+// lane p has the maximum and sum of the p-th, and the values of 16, or of the
+// last 4, are under way together.
+__device__ __forceinline__ Joined join_parts(const AttnArgs& a, int group, int row, int first, int step, int count) {
+    const int lane = threadIdx.x % kWave;
+    auto at = [&](int p) { return ((int64_t)group * 2 * a.workers + first + step * p) * a.rows + row; };
+    Joined r = {kNone, 0.0f, {0, 0, 0, 0}};
+    for (int p0 = 0; p0 < count; p0 += kWave) {
+        const int here = min(count - p0, kWave);
+        v2f stat = v2f{kNone, 0.0f};
+        if (lane < here) stat = *reinterpret_cast<const v2f*>(a.stats + 2 * at(p0 + lane));
+        float weight = 0.0f;
+        auto batch = [&](auto size, int p) {
+            constexpr int kSize = decltype(size)::value;
+            v2f x[kSize][2];
+#pragma unroll
+            for (int u = 0; u < kSize; ++u) {
+                const float* from = a.sums + at(p0 + min(p + u, here - 1)) * a.dim;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int d = 2 * lane + 128 * i;
+                    x[u][i] = d < a.dim ? *reinterpret_cast<const v2f*>(from + d) : v2f{0, 0};
+                }
+            }
+            if (p == 0) {
+                const float top = fmaxf(r.m, column_max(lanes_max<16>(stat.x))), zero_at = top == kNone ? 0.0f : top;
+                const float by = __builtin_amdgcn_exp2f(r.m - zero_at);
+                weight = __builtin_amdgcn_exp2f(stat.x - zero_at);
+                r.l = r.l * by + column_sum(lanes_sum<16>(stat.y * weight));
+                r.m = top;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r.o[i] *= by;
+            }
+#pragma unroll
+            for (int u = 0; u < kSize; ++u) {
+                const float w = p + u < here ? __uint_as_float(lane_of(__float_as_uint(weight), min(p + u, kWave - 1))) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r.o[i] = __builtin_fmaf(x[u][i / 2][i % 2], w, r.o[i]);
+            }
+        };
+        int p = 0;
+        for (; here - p > 4; p += 16) batch(std::integral_constant<int, 16>{}, p);
+        if (p < here) batch(std::integral_constant<int, 4>{}, p);
+    }
+    return r;
+}
+
+// Joins the partial sums of split sequences.  The n workgroups of a sequence's
+// n partial sums share its query heads: of up to kFew partial sums a wavefront
+// joins those of a head, of more the four wavefronts of a workgroup do, a
+// quarter each.
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+    constexpr int kFew = 4;
     __shared__ float part_max[kWaves], part_sum[kWaves];
     __shared__ float part_out[kWaves][QLIN_MAX_HEAD_DIM];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -501,51 +564,26 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
     if (record >= records) return;
     const int shared_by = a.heads / a.kv_heads, tile = group % a.tiles;
     const int rows = min(a.rows, shared_by - tile * kAttnHeads);
-    const int mine = (parts - wave + kWaves - 1) / kWaves;   // the wavefront's partial sums: wave, wave + 4, ..
-    for (int row = record - begin; row < rows; row += parts) {
-        auto at = [&](int p) { return ((int64_t)group * 2 * a.workers + begin + wave + kWaves * p) * a.rows + row; };
-        float m = kNone, l = 0.0f, o[4] = {0, 0, 0, 0};
-        for (int p0 = 0; p0 < mine; p0 += kWave) {
-            const int here = min(mine - p0, kWave);
-            v2f stat = v2f{kNone, 0.0f};
-            if (lane < here) stat = *reinterpret_cast<const v2f*>(a.stats + 2 * at(p0 + lane));
-            float weight = 0.0f;
-            auto batch = [&](auto count, int p) {   // the values of partial sums p .. p + count - 1, under way together
-                constexpr int kCount = decltype(count)::value;
-                v2f x[kCount][2];
+    const int64_t head0 = (int64_t)s * a.heads + group / a.tiles * shared_by + tile * kAttnHeads;
+    if (parts <= kFew) {
+        for (int row = kWaves * (record - begin) + wave; row < rows; row += kWaves * parts) {
+            const Joined r = join_parts(a, group, row, begin, 1, parts);
+            const float by = r.l > 0.0f || r.l != r.l ? 1.0f / r.l : 0.0f;
+            uint16_t* to = a.out + (head0 + row) * a.dim;
 #pragma unroll
-                for (int u = 0; u < kCount; ++u) {
-                    const float* from = a.sums + at(p0 + min(p + u, here - 1)) * a.dim;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int d = 2 * lane + 128 * i;
-                        x[u][i] = d < a.dim ? *reinterpret_cast<const v2f*>(from + d) : v2f{0, 0};
-                    }
-                }
-                if (p == 0) {
-                    const float top = fmaxf(m, column_max(lanes_max<16>(stat.x))), zero_at = top == kNone ? 0.0f : top;
-                    const float by = __builtin_amdgcn_exp2f(m - zero_at);
-                    weight = __builtin_amdgcn_exp2f(stat.x - zero_at);
-                    l = l * by + column_sum(lanes_sum<16>(stat.y * weight));
-                    m = top;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] *= by;
-                }
-#pragma unroll
-                for (int u = 0; u < kCount; ++u) {
-                    const float w = p + u < here ? __uint_as_float(lane_of(__float_as_uint(weight), min(p + u, kWave - 1))) : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[u][i / 2][i % 2], w, o[i]);
-                }
-            };
-            int p = 0;
-            for (; here - p > 4; p += 16) batch(std::integral_constant<int, 16>{}, p);
-            if (p < here) batch(std::integral_constant<int, 4>{}, p);
+            for (int i = 0; i < 2; ++i) {
+                const int d = 2 * lane + 128 * i;
+                if (d < a.dim) *reinterpret_cast<uint32_t*>(to + d) = bf16_pair(r.o[2 * i] * by, r.o[2 * i + 1] * by);
+            }
         }
+        return;
+    }
+    for (int row = record - begin; row < rows; row += parts) {
+        const Joined r = join_parts(a, group, row, begin + wave, kWaves, (parts - wave + kWaves - 1) / kWaves);
         __syncthreads();   // the buffers are free
-        if (lane == 0) part_max[wave] = m, part_sum[wave] = l;
+        if (lane == 0) part_max[wave] = r.m, part_sum[wave] = r.l;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part_out[wave][2 * lane + 128 * (i / 2) + i % 2] = o[i];
+        for (int i = 0; i < 4; ++i) part_out[wave][2 * lane + 128 * (i / 2) + i % 2] = r.o[i];
         __syncthreads();
         const int d = threadIdx.x;
         if (d < a.dim) {
@@ -559,8 +597,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
                 sum += part_sum[w] * by;
                 out += part_out[w][d] * by;
             }
-            const int head = group / a.tiles * shared_by + tile * kAttnHeads + row;
-            a.out[((int64_t)s * a.heads + head) * a.dim + d] = f32_to_bf16(sum > 0.0f || sum != sum ? out / sum : 0.0f);
+            a.out[(head0 + row) * a.dim + d] = f32_to_bf16(sum > 0.0f || sum != sum ? out / sum : 0.0f);
         }
     }
 }
@@ -589,10 +626,13 @@ constexpr int kCus = 256;
 }  // namespace
 
 AttnShape attn_shape(int heads, int kv_heads, int dim) {
-    const int resident = kCus * waves_per_simd(dim <= 64 ? 64 : dim <= 128 ? 128 : 256);
+    // Two workgroups to a CU (one of 256 channels), though the registers hold more: 8 x 32768 tokens of 32 / 8 heads of
+    // 128 in E4M3 take 101 us with two to a CU, 109 with three or one.  The room that is left takes the items beyond
+    // `workers`, of which there are up to S.
+    const int share = kCus * (dim <= 128 ? 2 : 1);
     const int shared_by = heads / kv_heads, tiles = (shared_by + kAttnHeads - 1) / kAttnHeads;
     const int groups = kv_heads * tiles;
-    return AttnShape{tiles, shared_by < kAttnHeads ? shared_by : kAttnHeads, groups >= resident ? 1 : resident / groups};
+    return AttnShape{tiles, shared_by < kAttnHeads ? shared_by : kAttnHeads, groups >= share ? 1 : share / groups};
 }
 
 int64_t attn_workspace(int heads, int kv_heads, int dim) {
@@ -628,11 +668,9 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.tiles = shape.tiles;
     a.rows = shape.rows;
     a.workers = shape.workers;
-    // There are up to workers + S items: one round of workgroups where the sequences are few beside them.  Where they are
-    // many, a sequence of 512 tokens is not cut (64 of 256 tokens, 32 / 8 heads of 128: 18.2 us cut in two, 13.4 whole).
-    const bool few = c.S <= shape.workers / 2;
-    a.items = few ? shape.workers - c.S : shape.workers;
-    a.least = few ? kAttnWaves : 4 * kAttnWaves;
+    // Where the sequences are many, one of 512 tokens is not cut (64 of 256 tokens, 32 / 8 heads of 128: 18.2 us cut in
+    // two, 13.4 whole).
+    a.least = c.S <= shape.workers / 2 ? kAttnWaves : 4 * kAttnWaves;
     a.scale = c.scale * 1.44269504088896340736f;
     const int64_t tokens = (int64_t)c.columns * c.cache.page_size, whole = (int64_t)c.S * groups;
     const bool alone = tokens <= (c.cache.dim <= 64 ? 512 : 256) || (tokens <= kMedium && whole >= kCus / 2) || c.S > kScanned;

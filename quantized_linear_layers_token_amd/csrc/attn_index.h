@@ -34,10 +34,17 @@ constexpr AttnSpan attn_span(int length, int columns, int page_size, int window)
     return AttnSpan{n, start, (unsigned)((n + kAttnUnit - 1) / kAttnUnit - start / kAttnUnit)};
 }
 
-// Units of an item at most; `least` (kAttnWaves or more) where the shares are smaller.
+// Units of an item at most, a multiple of the wavefronts (which share them
+// evenly then); `least` (a multiple too) where the shares are smaller.
 constexpr unsigned attn_most(int64_t total, int workers, int least) {
-    const int64_t even = (total + workers - 1) / workers;
-    return even < least ? (unsigned)least : even > 0x7fffffff ? 0x7fffffffu : (unsigned)even;
+    const int64_t even = ((total + workers - 1) / workers + kAttnWaves - 1) / kAttnWaves * kAttnWaves;
+    return even < least ? (unsigned)least : even > 0x7ffffff0 ? 0x7ffffff0u : (unsigned)even;
+}
+// The next try where that gave `items`, more than workers: a multiple of the
+// wavefronts again, and larger.
+constexpr unsigned attn_larger(unsigned most, unsigned items, int workers) {
+    const int64_t scaled = ((int64_t)most * items / workers + kAttnWaves) / kAttnWaves * kAttnWaves;
+    return scaled > 0x7ffffff0 ? 0x7ffffff0u : scaled > most ? (unsigned)scaled : most + kAttnWaves;
 }
 // Items of a sequence.
 constexpr unsigned attn_items(unsigned units, unsigned most) { return (units + most - 1) / most; }

@@ -2,8 +2,9 @@
 // and rotation of the heads, keys and values rounded into the paged cache (one
 // launch for the three), and cache rows read back.
 //
-// A workgroup takes one token: the cosines and sines of its position are
-// formed once, by dims / 2 threads, and shared by all of its heads through LDS.
+// A workgroup takes one token, or as many as its threads hold at once where the
+// heads are few: the cosines and sines of a position are formed once, by
+// dims / 2 threads, and shared by all of its heads through LDS.
 // LANES lanes hold a head, eight channels each, so that the sum of squares and
 // the absmax are reductions within 8, 16 or 32 lanes.  A lane's channels are
 // two runs of four: both channels of each of its pairs, so that nothing is
@@ -34,13 +35,16 @@ __device__ __forceinline__ float2 turn(int position, double frequency, float str
     return make_float2(c * strength, s * strength);
 }
 
-template <int LANES, int KIND, bool ROTATE, bool NEIGHBOURS>
+// TOKENS: those of a workgroup; more than one only where a token's heads take
+// at most kThreads / TOKENS threads.
+template <int LANES, int KIND, bool ROTATE, bool NEIGHBOURS, int TOKENS>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
-    __shared__ float2 turns[QLIN_MAX_HEAD_DIM / 2];
-    constexpr int kPer = kThreads / LANES;   // heads that the workgroup takes at once
-    const int64_t t = blockIdx.x;
-    const int c = threadIdx.x % LANES, first = threadIdx.x / LANES;
-    const bool mine = c < a.dim / 8;
+    extern __shared__ float2 turns[];        // [TOKENS][dims / 2]
+    constexpr int kPer = kThreads / LANES / TOKENS;   // heads of a token that the workgroup takes at once
+    const int c = threadIdx.x % LANES, first = threadIdx.x / LANES % kPer;
+    const int of = TOKENS > 1 ? threadIdx.x / LANES / kPer : 0;   // the thread's token
+    const int64_t t = (int64_t)blockIdx.x * TOKENS + of;
+    const bool mine = c < a.dim / 8 && (TOKENS == 1 || t < a.T);
     // the lane's channels: lo .. lo + 3 and hi .. hi + 3
     const int pairs = ROTATE ? a.rope.dims / 2 : 0;
     int lo = 8 * c, hi = 8 * c + 4;
@@ -57,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
         if (a.q_gamma) gamma[0][0] = *reinterpret_cast<const v2u*>(a.q_gamma + lo), gamma[0][1] = *reinterpret_cast<const v2u*>(a.q_gamma + hi);
         if (a.k_gamma) gamma[1][0] = *reinterpret_cast<const v2u*>(a.k_gamma + lo), gamma[1][1] = *reinterpret_cast<const v2u*>(a.k_gamma + hi);
     }
-    const int slot = a.kv_heads ? a.slots[t] : -1;
+    const int slot = a.kv_heads && (TOKENS == 1 || t < a.T) ? a.slots[t] : -1;
     int64_t row0 = -1;    // row of the cache of the token's first head
     float2 w[4];
 
@@ -77,11 +81,18 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
         }
         if (base == 0) {
             if constexpr (ROTATE) {
-                if (threadIdx.x < pairs) turns[threadIdx.x] = turn(a.positions[t], a.rope.frequencies[threadIdx.x], a.rope.strength);
+                if constexpr (TOKENS == 1) {
+                    if (threadIdx.x < pairs) turns[threadIdx.x] = turn(a.positions[t], a.rope.frequencies[threadIdx.x], a.rope.strength);
+                } else {
+                    for (int i = threadIdx.x; i < TOKENS * pairs; i += kThreads) {
+                        const int64_t token = (int64_t)blockIdx.x * TOKENS + i / pairs;
+                        if (token < a.T) turns[i] = turn(a.positions[token], a.rope.frequencies[i % pairs], a.rope.strength);
+                    }
+                }
                 __syncthreads();
                 if (turned) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = turns[4 * c + i];
+                    for (int i = 0; i < 4; ++i) w[i] = turns[of * pairs + 4 * c + i];
                 }
             }
             if (slot >= 0 && slot < a.cache.pages * a.cache.page_size)
@@ -226,12 +237,23 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(qlin_kv_cache a, c
     }
 }
 
+template <int LANES, int KIND, int TOKENS>
+void launch_tokens(const HeadsCall& c, hipStream_t st) {
+    const dim3 grid((unsigned)((c.T + TOKENS - 1) / TOKENS)), block(kThreads);
+    const size_t lds = c.rope.frequencies ? (size_t)TOKENS * (c.rope.dims / 2) * sizeof(float2) : 0;
+    if (!c.rope.frequencies) hipLaunchKernelGGL((heads_kernel<LANES, KIND, false, false, TOKENS>), grid, block, lds, st, c);
+    else if (c.rope.interleaved) hipLaunchKernelGGL((heads_kernel<LANES, KIND, true, true, TOKENS>), grid, block, lds, st, c);
+    else hipLaunchKernelGGL((heads_kernel<LANES, KIND, true, false, TOKENS>), grid, block, lds, st, c);
+}
+// Several tokens to a workgroup where its threads hold their heads at once and
+// the workgroups are still many: 32768 tokens of one kv head of 64 channels
+// written in 5.1 us with 16, 32.0 with one.
 template <int LANES, int KIND>
 void launch_lanes(const HeadsCall& c, hipStream_t st) {
-    const dim3 grid((unsigned)c.T), block(kThreads);
-    if (!c.rope.frequencies) hipLaunchKernelGGL((heads_kernel<LANES, KIND, false, false>), grid, block, 0, st, c);
-    else if (c.rope.interleaved) hipLaunchKernelGGL((heads_kernel<LANES, KIND, true, true>), grid, block, 0, st, c);
-    else hipLaunchKernelGGL((heads_kernel<LANES, KIND, true, false>), grid, block, 0, st, c);
+    const int threads = (c.heads + 2 * c.kv_heads) * LANES;
+    if (16 * threads <= kThreads && c.T >= 8192) launch_tokens<LANES, KIND, 16>(c, st);
+    else if (4 * threads <= kThreads && c.T >= 1024) launch_tokens<LANES, KIND, 4>(c, st);
+    else launch_tokens<LANES, KIND, 1>(c, st);
 }
 template <int KIND>
 void launch_kind(const HeadsCall& c, hipStream_t st) {

@@ -24,12 +24,12 @@ __device__ __forceinline__ v4u add8(const v4u& a, const v4u& b) {
 
 // THREADS lanes per row, ROWS rows per workgroup (more than one only for rows
 // of one wavefront); CPT 16-byte chunks of the row per thread.
+constexpr int kLongThreads = 1024;
+
 template <int THREADS, int ROWS, int CPT, int OUT>
 __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
     static_assert(ROWS == 1 || THREADS == kWave, "a row of several wavefronts takes the workgroup's barrier");
     constexpr int kWaves = THREADS / kWave;
-    constexpr bool kKeepGamma = CPT <= 4;   // held for the second use where registers allow, else read again
-    constexpr int kBatch = CPT < 4 ? CPT : 4;   // chunks whose loads are under way together
     __shared__ float red[2 * kWaves];
     const int tid = ROWS > 1 ? threadIdx.x % THREADS : threadIdx.x;
     const int64_t m = ROWS > 1 ? (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS : blockIdx.x;
@@ -40,48 +40,35 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
     const v4u* gamma = reinterpret_cast<const v4u*>(a.gamma);
     const v4u zero = v4u{0, 0, 0, 0};
 
-    v4u r[CPT], g[kKeepGamma ? CPT : 1];
-    if constexpr (kKeepGamma) {
+    v4u r[CPT], g[CPT];
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+        const int c = tid + j * THREADS;
+        r[j] = c < nchunks ? x[c] : zero;
+        g[j] = c < nchunks ? gamma[c] : zero;
+    }
+    if (res) {
+        v4u* sum = reinterpret_cast<v4u*>(a.sum + m * a.K);
+        v4u b[CPT];
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
             const int c = tid + j * THREADS;
-            g[j] = c < nchunks ? gamma[c] : zero;
+            b[j] = c < nchunks ? res[c] : zero;
         }
-    }
 #pragma unroll
-    for (int j0 = 0; j0 < CPT; j0 += kBatch) {
-#pragma unroll
-        for (int j = j0; j < j0 + kBatch; ++j) {
+        for (int j = 0; j < CPT; ++j) {
             const int c = tid + j * THREADS;
-            r[j] = c < nchunks ? x[c] : zero;
-        }
-        if (res) {
-            v4u* sum = reinterpret_cast<v4u*>(a.sum + m * a.K);
-            v4u b[kBatch];
-#pragma unroll
-            for (int j = j0; j < j0 + kBatch; ++j) {
-                const int c = tid + j * THREADS;
-                b[j - j0] = c < nchunks ? res[c] : zero;
-            }
-#pragma unroll
-            for (int j = j0; j < j0 + kBatch; ++j) {
-                const int c = tid + j * THREADS;
-                r[j] = add8(r[j], b[j - j0]);
-                if (c < nchunks) sum[c] = r[j];
-            }
+            r[j] = add8(r[j], b[j]);
+            if (c < nchunks) sum[c] = r[j];
         }
     }
 
     float squares = 0.0f, amax = 0.0f, group[OUT == kNormFp8Block ? CPT : 1];
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
-        const int c = tid + j * THREADS;
-        v4u gj;
-        if constexpr (kKeepGamma) gj = g[j];
-        else gj = c < nchunks ? gamma[c] : zero;
         float f[8], w[8], top = 0.0f;
         widen8(r[j], f);
-        widen8(gj, w);
+        widen8(g[j], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares);
         if constexpr (OUT != kNormBf16) {
@@ -113,12 +100,9 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
     for (int j = 0; j < CPT; ++j) {
         const int c = tid + j * THREADS;
         if (c >= nchunks) break;
-        v4u gj;
-        if constexpr (kKeepGamma) gj = g[j];
-        else gj = gamma[c];
         float f[8], w[8];
         widen8(r[j], f);
-        widen8(gj, w);
+        widen8(g[j], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= w[i];
         if constexpr (OUT == kNormBf16) {
@@ -135,6 +119,69 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
     }
 }
 
+// Rows longer than a workgroup's registers hold: read twice, the second time
+// from the caches (the row, or the sum that the first pass wrote).
+template <int OUT>
+__global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormCall a) {
+    constexpr int kWaves = kLongThreads / kWave;
+    constexpr bool kFp8 = OUT == kNormFp8 || OUT == kNormFp8Block;
+    __shared__ float red[2 * kWaves];
+    const int tid = threadIdx.x, nchunks = (int)(a.K >> 3);
+    const int64_t m = blockIdx.x;
+    const v4u* x = reinterpret_cast<const v4u*>(a.x + m * a.K);
+    const v4u* res = a.residual ? reinterpret_cast<const v4u*>(a.residual + m * a.K) : nullptr;
+    const v4u* gamma = reinterpret_cast<const v4u*>(a.gamma);
+    v4u* sum = reinterpret_cast<v4u*>(a.sum + m * a.K);
+    float squares = 0.0f, amax = 0.0f;
+    for (int c = tid; c < nchunks; c += kLongThreads) {
+        v4u r = x[c];
+        if (res) r = add8(r, res[c]), sum[c] = r;
+        float f[8], w[8];
+        widen8(r, f);
+        widen8(gamma[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares), amax = fmaxf(amax, fabsf(f[i] * w[i]));
+    }
+    squares = wave_sum_f32(squares);
+    amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
+    if (tid % kWave == 0) red[tid / kWave] = squares, red[kWaves + tid / kWave] = amax;
+    __syncthreads();
+    squares = red[0], amax = red[kWaves];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) squares += red[w], amax = fmaxf(amax, red[kWaves + w]);
+    const float d = 1.0f / sqrtf(squares / (float)a.K + a.eps);
+    Rounding rr = rounding<kFp8>(amax);
+    if (OUT != kNormBf16 && OUT != kNormFp8Block && tid == 0) a.s[m] = scale_of<kFp8>(amax * d);
+    const v4u* row = res ? sum : x;
+    const int turns = (nchunks + kLongThreads - 1) / kLongThreads;
+    for (int k = 0; k < turns; ++k) {          // (whole groups of 16 lanes stay together: their maximum is taken)
+        const int c = tid + k * kLongThreads;
+        float f[8] = {}, w[8];
+        if (c < nchunks) {
+            widen8(row[c], f);
+            widen8(gamma[c], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= w[i];
+        }
+        if constexpr (OUT == kNormFp8Block) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+            top = lanes_max<16>(top);
+            rr = rounding<true>(top);
+            if (c < nchunks && c % 16 == 0) a.s[m * (a.K / 128) + c / 16] = scale_of<true>(top * d);
+        }
+        if (c >= nchunks) continue;
+        if constexpr (OUT == kNormBf16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= d;
+            reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.y) + m * a.K)[c] = narrow8(f);
+        } else {
+            reinterpret_cast<v2u*>(static_cast<uint8_t*>(a.y) + m * a.K)[c] = codes8<kFp8>(f, rr);
+        }
+    }
+}
+
 template <int OUT>
 hipError_t launch_out(const NormCall& c, hipStream_t st) {
     const int64_t chunks = c.K / 8;
@@ -146,8 +193,6 @@ hipError_t launch_out(const NormCall& c, hipStream_t st) {
     integral_constant<int, 1> one;
     integral_constant<int, 2> two;
     integral_constant<int, 4> four;
-    integral_constant<int, 8> eight;
-    integral_constant<int, 16> sixteen;
     integral_constant<int, 64> t64;
     integral_constant<int, 256> t256;
     integral_constant<int, 1024> t1024;
@@ -156,8 +201,7 @@ hipError_t launch_out(const NormCall& c, hipStream_t st) {
     else if (chunks <= 512) go(t256, one, two);
     else if (chunks <= 1024) go(t256, one, four);
     else if (chunks <= 4096) go(t1024, one, four);
-    else if (chunks <= 8192) go(t1024, one, eight);
-    else go(t1024, one, sixteen);
+    else hipLaunchKernelGGL(norm_long_kernel<OUT>, dim3((unsigned)c.M), dim3(kLongThreads), 0, st, c);
     return hipGetLastError();
 }
 

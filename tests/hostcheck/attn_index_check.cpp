@@ -43,7 +43,15 @@ int main() {
             total += span[s].units;
             CHECK((span[s].units == 0) == (length[s] <= 0 || columns == 0));
         }
-        const unsigned most = attn_most(total, workers, kAttnWaves * draw(1, 4));
+        unsigned most = attn_most(total, workers, kAttnWaves * draw(1, 4));
+        for (int k = S < workers ? draw(0, 6) : 0; k > 0; --k) {       // (as the workgroups look for a size that fits)
+            unsigned n = 0;
+            for (int s = 0; s < S; ++s) n += attn_items(span[s].units, most);
+            if (n <= (unsigned)workers) break;
+            const unsigned next = attn_larger(most, n, workers);
+            CHECK(next > most && next % kAttnWaves == 0);
+            most = next;
+        }
         unsigned items = 0, split = 0;
         std::vector<std::vector<int>> taken(S);
         for (int s = 0; s < S; ++s) {

@@ -42,6 +42,7 @@ ROPE = [  # T, heads, dim, dims, interleaved, norm
     (7, 1, 80, 80, False, True), (9, 5, 80, 48, True, True), (5, 7, 96, 16, False, False), (4, 32, 128, 128, False, True),
     (3, 40, 128, 64, False, False), (11, 33, 128, 112, True, True), (2, 9, 144, 144, False, True), (3, 17, 256, 256, True, False),
     (2, 3, 256, 96, False, True), (70, 4, 128, 128, False, False),
+    (1030, 1, 128, 64, False, True), (2050, 2, 64, 64, True, False), (16390, 1, 48, 32, False, False), (1025, 3, 256, 256, False, False),   # several tokens to a workgroup
 ]
 
 
@@ -77,7 +78,7 @@ WRITE = [  # T, heads, kv_heads, dim, page, dims (0: no rotation), interleaved, 
     (1, 4, 1, 128, 16, 128, False, False), (5, 0, 2, 64, 48, 0, False, False), (9, 3, 3, 16, 16, 16, True, True),
     (33, 32, 8, 128, 64, 128, False, True), (6, 10, 5, 80, 32, 48, False, False), (4, 8, 2, 256, 16, 256, True, True),
     (7, 0, 4, 96, 16, 96, False, True), (12, 6, 6, 144, 80, 64, True, False), (3, 64, 8, 128, 16, 0, False, True),
-    (2, 200, 100, 64, 16, 64, False, False),
+    (2, 200, 100, 64, 16, 64, False, False), (1027, 2, 1, 64, 16, 64, False, True), (4099, 0, 1, 64, 48, 0, False, False),
 ]
 
 

@@ -103,8 +103,9 @@ def test_norm(kind, M, K):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_residual_updated_in_place(kind):
-    case = inputs(2, 21, 1024)
-    check(kind, *case, run(kind, *case, in_place=True))
+    for M, K in ((21, 1024), (2, 40960)):
+        case = inputs(2, M, K)
+        check(kind, *case, run(kind, *case, in_place=True))
 
 
 @pytest.mark.parametrize("kind", KINDS)
