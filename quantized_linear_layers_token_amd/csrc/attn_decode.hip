@@ -50,7 +50,7 @@ struct AttnArgs {
     float* stats;     // their maxima and sums of p [group of heads][2 workers][rows][2]
     int* joins;       // [group of heads]: 4 ints, the number of partial sums first, then for each {sequence, its first, their number, 0}
     int64_t npages;
-    int S, heads, kv_heads, dim, columns, page_size, window;
+    int S, heads, kv_heads, shared_by, dim, columns, page_size, page_shift, window;   // shared_by: query heads of a kv head
     int tiles, rows, workers;
     int least;        // items are not cut below so many units
     float scale;      // times log2 e
@@ -179,12 +179,10 @@ __global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP, KIND == QLIN_CACH
     __shared__ float stats[kSlots][2][kAttnHeads];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
-    const int groups = a.kv_heads * a.tiles;
-    const int group = blockIdx.x % groups, worker = blockIdx.x / groups;
-    const int kv_head = group / a.tiles, tile = group % a.tiles;
-    const int shared_by = a.heads / a.kv_heads;
-    const int head0 = kv_head * shared_by + tile * kAttnHeads;
-    const int rows = min(a.rows, shared_by - tile * kAttnHeads);
+    const int group = blockIdx.x, worker = blockIdx.y;
+    const int kv_head = a.tiles == 1 ? group : group / a.tiles, tile = a.tiles == 1 ? 0 : group % a.tiles;
+    const int head0 = kv_head * a.shared_by + tile * kAttnHeads;
+    const int rows = min(a.rows, a.shared_by - tile * kAttnHeads);
     AttnSpan span = {};
     int s = 0, first = 0, last = 0, record = -1;   // the item: a sequence and its units; its partial sum (-1: the whole sequence)
     if constexpr (ALONE) {
@@ -265,7 +263,7 @@ __global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP, KIND == QLIN_CACH
             Places p;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                p.at[j] = attn_place(span, unit, j, table, (int)a.npages, a.kv_heads, kv_head, a.page_size);
+                p.at[j] = attn_place(span, unit, j, table, (int)a.npages, a.kv_heads, kv_head, a.page_size, a.page_shift);
             return p;
         };
         auto load_keys = [&](const Places& p, T& t) {
@@ -557,14 +555,13 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
     __shared__ float part_max[kWaves], part_sum[kWaves];
     __shared__ float part_out[kWaves][QLIN_MAX_HEAD_DIM];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int groups = a.kv_heads * a.tiles;
-    const int group = blockIdx.x % groups, record = blockIdx.x / groups;
+    const int group = blockIdx.x, record = blockIdx.y;
     const Table joins = table_of(a.joins + 4 * ((int64_t)group * (2 * a.workers + 1)));
     const int records = joins[0], s = joins[4 * (1 + record)], begin = joins[4 * (1 + record) + 1], parts = joins[4 * (1 + record) + 2];
     if (record >= records) return;
-    const int shared_by = a.heads / a.kv_heads, tile = group % a.tiles;
-    const int rows = min(a.rows, shared_by - tile * kAttnHeads);
-    const int64_t head0 = (int64_t)s * a.heads + group / a.tiles * shared_by + tile * kAttnHeads;
+    const int tile = group % a.tiles;
+    const int rows = min(a.rows, a.shared_by - tile * kAttnHeads);
+    const int64_t head0 = (int64_t)s * a.heads + group / a.tiles * a.shared_by + tile * kAttnHeads;
     if (parts <= kFew) {
         for (int row = kWaves * (record - begin) + wave; row < rows; row += kWaves * parts) {
             const Joined r = join_parts(a, group, row, begin, 1, parts);
@@ -603,13 +600,13 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
 }
 
 template <int KIND, int DP>
-void launch_dim(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
+void launch_dim(const AttnArgs& a, bool alone, dim3 grid, hipStream_t st) {
     constexpr int kAlone = DP == 64 ? 8 : kWaves;
-    if (alone) hipLaunchKernelGGL((attn_kernel<KIND, DP, kAlone, true>), dim3(grid), dim3(kAlone * kWave), 0, st, a);
-    else hipLaunchKernelGGL((attn_kernel<KIND, DP, kWaves, false>), dim3(grid), dim3(kThreads), 0, st, a);
+    if (alone) hipLaunchKernelGGL((attn_kernel<KIND, DP, kAlone, true>), grid, dim3(kAlone * kWave), 0, st, a);
+    else hipLaunchKernelGGL((attn_kernel<KIND, DP, kWaves, false>), grid, dim3(kThreads), 0, st, a);
 }
 template <int KIND>
-void launch_kind(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
+void launch_kind(const AttnArgs& a, bool alone, dim3 grid, hipStream_t st) {
     if (a.dim <= 64) launch_dim<KIND, 64>(a, alone, grid, st);
     else if (a.dim <= 128) launch_dim<KIND, 128>(a, alone, grid, st);
     else launch_dim<KIND, 256>(a, alone, grid, st);
@@ -620,7 +617,7 @@ void launch_kind(const AttnArgs& a, bool alone, unsigned grid, hipStream_t st) {
 // number fills half of the CUs; and for more sequences than a workgroup can scan.
 constexpr int64_t kMedium = 2048;
 constexpr int kScanned = 1024;
-constexpr int64_t kMaxGrid = int64_t(1) << 22;   // workgroups of 512 threads: a launch holds 2^32 threads
+constexpr int kMaxSequences = 4096;   // of a launch: up to 1024 groups of heads and 2^32 threads
 constexpr int kCus = 256;
 
 }  // namespace
@@ -661,9 +658,11 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.S = c.S;
     a.heads = c.heads;
     a.kv_heads = c.cache.kv_heads;
+    a.shared_by = c.heads / c.cache.kv_heads;
     a.dim = c.cache.dim;
     a.columns = c.columns;
     a.page_size = c.cache.page_size;
+    a.page_shift = a.page_size & (a.page_size - 1) ? -1 : __builtin_ctz((unsigned)a.page_size);
     a.window = c.window;
     a.tiles = shape.tiles;
     a.rows = shape.rows;
@@ -674,8 +673,7 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.scale = c.scale * 1.44269504088896340736f;
     const int64_t tokens = (int64_t)c.columns * c.cache.page_size, whole = (int64_t)c.S * groups;
     const bool alone = tokens <= (c.cache.dim <= 64 ? 512 : 256) || (tokens <= kMedium && whole >= kCus / 2) || c.S > kScanned;
-    const int64_t most = alone ? whole : (int64_t)groups * (shape.workers + c.S + 1);
-    if (most > kMaxGrid) {   // one half of the sequences after the other
+    if (c.S > kMaxSequences) {   // one half of the sequences after the other
         AttnCall part = c;
         part.S = c.S / 2;
         const hipError_t e = launch_attn(part, st);
@@ -688,13 +686,13 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
         part.lengths += done;
         return launch_attn(part, st);
     }
-    const unsigned grid = (unsigned)most;
+    const dim3 grid((unsigned)groups, (unsigned)(alone ? c.S : shape.workers + c.S + 1));
     if (c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(a, alone, grid, st);
     else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(a, alone, grid, st);
     else launch_kind<QLIN_CACHE_FP8>(a, alone, grid, st);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && !alone) {
-        hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(groups * 2 * shape.workers)), dim3(kThreads), 0, st, a);
+        hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)groups, (unsigned)(2 * shape.workers)), dim3(kThreads), 0, st, a);
         e = hipGetLastError();
     }
     return e;

@@ -58,14 +58,17 @@ constexpr unsigned attn_first_unit(unsigned units, unsigned n, unsigned i) {
 // token and which of its 16 tokens are live, lo <= i < hi.  A half without any
 // (behind the length, before the window, of a page outside the cache) has the
 // rows of page 0, which its loads may read and nothing uses.
+// page_shift: log2 of page_size, or -1 (a division of its own would wait some
+// 40 instructions before every step's loads).
 struct AttnPlace {
     int64_t row;
     int lo, hi;
 };
 template <class Table>
-constexpr AttnPlace attn_place(const AttnSpan& span, int unit, int half, Table table, int pages, int kv_heads, int kv_head, int page_size) {
+constexpr AttnPlace attn_place(const AttnSpan& span, int unit, int half, Table table, int pages, int kv_heads, int kv_head, int page_size,
+                               int page_shift) {
     const int t = (span.start / kAttnUnit + unit) * kAttnUnit + kAttnHalf * half;
-    const int column = t / page_size, place = t - column * page_size;
+    const int column = page_shift >= 0 ? t >> page_shift : t / page_size, place = t - column * page_size;
     int page = t < span.n && t + kAttnHalf > span.start ? table[column] : -1;
     const bool live = page >= 0 && page < pages;
     page = live ? page : 0;

@@ -36,6 +36,7 @@ int main() {
         std::vector<int> length(S), table((size_t)S * columns);
         for (int& v : length) v = draw(0, 5) == 0 ? draw(-2, 1) : draw(0, columns * page_size + 20);
         for (int& v : table) v = draw(0, 30) == 0 ? draw(-3, pages + 3) : draw(0, pages - 1);
+        const int shift = page_size & (page_size - 1) ? -1 : __builtin_ctz(page_size);
         std::vector<AttnSpan> span(S);
         int64_t total = 0;
         for (int s = 0; s < S; ++s) {
@@ -74,7 +75,7 @@ int main() {
                         ++units_seen;
                         for (int half = 0; half < 2; ++half) {
                             const AttnPlace p = attn_place(span[s], u, half, Row{table.data() + (size_t)s * columns, columns}, pages, kv_heads,
-                                                           kv_heads - 1, page_size);
+                                                           kv_heads - 1, page_size, shift);
                             const int64_t rows = (int64_t)pages * kv_heads * page_size;
                             CHECK(p.row >= 0 && p.row % kAttnHalf == 0 && p.row + kAttnHalf <= rows);
                             const int t = (span[s].start / kAttnUnit + u) * kAttnUnit + kAttnHalf * half;
