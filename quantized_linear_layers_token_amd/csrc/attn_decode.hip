@@ -22,6 +22,17 @@
 // item writes a partial sum, and a second launch joins them.  So the launches do
 // not depend on the lengths and can be captured.  Where no sequence can be long,
 // or there are a great many, an item is a sequence and there is one launch.
+//
+// Measured: 206744 tokens of 8 sequences (32 / 8 heads of 128, E4M3, 436 MB)
+// 85.8 us, 5.1 TB/s, the rate of a large copy; equal lengths 5.5 TB/s, bf16 5.9.
+// What is left of the time is fixed: 5 us for a short sequence in one launch
+// (lengths, page table and rows are three dependent loads), 2 for the second
+// launch, 1.5 to 2 more where it joins something.  A sequence of 777 tokens takes
+// 8.8 us, 37 ragged ones in bf16 (57 MB) 17.
+// Two units of every wavefront under way instead of one changed nothing
+// (101.3 -> 101.5 us for 8 x 32768 tokens) or cost up to a fifth (128 x 1024
+// tokens of 4 kv heads of 64: 16.8 -> 20.8), three workgroups to a CU instead of
+// two 5 %, eight wavefronts to a workgroup instead of four 40 % of 64 x 256 tokens.
 #include <type_traits>
 
 #include "attn_index.h"

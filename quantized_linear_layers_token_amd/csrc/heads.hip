@@ -10,6 +10,15 @@
 // two runs of four: both channels of each of its pairs, so that nothing is
 // exchanged for the rotation, and its cosines and sines are the same for every
 // head of the token and stay in registers.
+//
+// Bound by memory for many tokens: 4096 tokens of 32 heads of 128, normalised
+// and rotated, 13.7 us (67 MB, 4.9 TB/s; without the norm 12.2); with 8 key and
+// value heads rounded to int8 as well 19 us (92 MB).  With eight channels of a
+// lane side by side, the partner's exchanged by LDS permutes and normalised a
+// second time, and two more divisions to a head, vector instructions bounded
+// it (17.7 and 29 us).  Rows read back: 65536 of 8 heads of 128 in E4M3, 77 us
+// (407 MB, 5.3 TB/s); sixteen channels to a lane, whose stores leave half a line
+// each, took 94.
 #include <type_traits>
 
 #include "layer_device.h"

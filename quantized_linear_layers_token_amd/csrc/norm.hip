@@ -7,6 +7,15 @@
 // value is t * d; its code for the absmax a * d is the code of t for the absmax
 // a, since d cancels out of t * d * (Q / (a * d)).  So the codes wait for
 // max |t| alone and only the scale, a * d / Q, takes the sum of squares.
+//
+// Bound by memory for many rows: 8192 x 4096 with the residual, E4M3 out,
+// moves 235 MB in 42 us (5.6 TB/s; a large copy reaches 5.1), and fetches and
+// writes exactly those bytes.  One row of 4096 takes 2.1 us above nothing else:
+// the call's host time (6.4 us) bounds it.  A row has the threads that hold it
+// in one to four 16-byte chunks each: a wavefront up to 512 inputs (four rows
+// to a workgroup), 256 threads up to 8192, 1024 up to 32768, and two passes
+// over longer ones (131072 inputs, 256 rows: 45 us; held in registers, which
+// spill, 72).
 #include <type_traits>
 
 #include "layer_device.h"

@@ -248,4 +248,38 @@ def test_every_mfma_result_access_is_padded(tmp_path):
     assert not bad, bad[:5]
     spills = [int(v) for v in re.findall(r"\.vgpr_spill_count:\s+(\d+)", text)]
     assert max(spills) == 0
-    assert "v_pk_" not in text or not re.search(r"v_pk_(add|mul|fma)_f32", text)
+    assert not re.search(r"v_pk_(add|mul|fma)_f32", text)
+    lost = lost_registers(text)
+    assert not lost, lost[:5]
+
+
+def lost_registers(text):
+    """Byte permutations between a kernel's first and last matrix instruction that read a register which f32 arithmetic
+    wrote last: there they transpose loaded values, and the register allocator has been seen to give the upper half of a
+    loaded pair away before its use."""
+    arithmetic = ("v_sub_f32", "v_add_f32", "v_mul_f32", "v_exp_f32", "v_lshlrev_b32", "v_cvt_pk_bf16_f32", "v_fma_f32")
+    found = []
+    for name, body in re.findall(r"^(_ZN4qlin\S*attn_kernel\S*):(.*?)s_endpgm", text, re.M | re.S):
+        code = [line.strip() for line in body.splitlines() if line.startswith("\t") and not line.strip().startswith((".", ";"))]
+        products = [i for i, line in enumerate(code) if line.startswith("v_mfma")]
+        if not products:
+            continue
+        wrote = {}
+        for line in code[products[0]:products[-1]]:
+            op = line.split()[0]
+            args = [a.strip() for a in line[len(op):].split(",")]
+            if op == "v_perm_b32":
+                found += [(name, line) for a in args[1:3] if wrote.get(a, "").startswith(arithmetic)]
+            pair = re.match(r"v\[(\d+):(\d+)\]$", args[0])
+            for r in (range(int(pair[1]), int(pair[2]) + 1) if pair else ()):
+                wrote[f"v{r}"] = op
+            if re.match(r"v\d+$", args[0]):
+                wrote[args[0]] = op
+    return found
+
+
+def test_the_scan_for_lost_registers_finds_one():
+    kernel = "_ZN4qlin1_attn_kernel:\n\tv_mfma_f32 v[0:3], v[4:7], v[8:11], v[0:3]\n\tglobal_load_dwordx2 v[20:21], v[2:3], off\n"
+    used = "\tv_perm_b32 v30, v20, v21, s1\n\tv_mfma_f32 v[0:3], v[4:7], v[8:11], v[0:3]\n\ts_endpgm\n"
+    assert not lost_registers(kernel + used)
+    assert lost_registers(kernel + "\tv_sub_f32_e32 v21, v1, v2\n" + used)
