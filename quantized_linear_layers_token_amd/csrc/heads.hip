@@ -273,11 +273,22 @@ void launch_kind(const HeadsCall& c, hipStream_t st) {
 
 }  // namespace
 
+// A launch holds 2^32 threads: many tokens take several.
 hipError_t launch_heads(const HeadsCall& c, hipStream_t st) {
-    if (c.kv_heads == 0 || c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(c, st);
-    else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(c, st);
-    else launch_kind<QLIN_CACHE_FP8>(c, st);
-    return hipGetLastError();
+    constexpr int64_t kTokens = int64_t(1) << 23;
+    for (int64_t t = 0; t < c.T; t += kTokens) {
+        HeadsCall part = c;
+        part.T = c.T - t < kTokens ? c.T - t : kTokens;
+        if (c.heads) part.q += t * c.q_stride, part.q_out += t * c.q_out_stride;
+        if (c.kv_heads) part.k += t * c.k_stride, part.v += t * c.v_stride, part.slots += t;
+        if (c.positions) part.positions += t;
+        if (c.kv_heads == 0 || c.cache.kind == QLIN_CACHE_BF16) launch_kind<QLIN_CACHE_BF16>(part, st);
+        else if (c.cache.kind == QLIN_CACHE_INT8) launch_kind<QLIN_CACHE_INT8>(part, st);
+        else launch_kind<QLIN_CACHE_FP8>(part, st);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_cache_read(const qlin_kv_cache& cache, const int* slots, int64_t n, uint16_t* k, uint16_t* v, hipStream_t st) {

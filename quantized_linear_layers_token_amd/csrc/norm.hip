@@ -216,13 +216,27 @@ hipError_t launch_out(const NormCall& c, hipStream_t st) {
 
 }  // namespace
 
+// A launch holds 2^32 threads: many rows take several.
 hipError_t launch_norm(NormOut out, const NormCall& c, hipStream_t st) {
-    switch (out) {
-        case kNormBf16: return launch_out<kNormBf16>(c, st);
-        case kNormInt8: return launch_out<kNormInt8>(c, st);
-        case kNormFp8: return launch_out<kNormFp8>(c, st);
-        default: return launch_out<kNormFp8Block>(c, st);
+    constexpr int64_t kRows = int64_t(1) << 21;
+    const int64_t codes = out == kNormBf16 ? 2 : 1, scales = out == kNormFp8Block ? c.K / 128 : 1;
+    for (int64_t m = 0; m < c.M; m += kRows) {
+        NormCall part = c;
+        part.M = c.M - m < kRows ? c.M - m : kRows;
+        part.x += m * c.K;
+        if (c.residual) part.residual += m * c.K, part.sum += m * c.K;
+        part.y = static_cast<uint8_t*>(c.y) + m * c.K * codes;
+        if (c.s) part.s += m * scales;
+        hipError_t e;
+        switch (out) {
+            case kNormBf16: e = launch_out<kNormBf16>(part, st); break;
+            case kNormInt8: e = launch_out<kNormInt8>(part, st); break;
+            case kNormFp8: e = launch_out<kNormFp8>(part, st); break;
+            default: e = launch_out<kNormFp8Block>(part, st);
+        }
+        if (e != hipSuccess) return e;
     }
+    return hipSuccess;
 }
 
 }  // namespace qlin
