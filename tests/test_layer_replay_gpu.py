@@ -172,3 +172,39 @@ def test_two_graphs_at_once():
             torch.cuda.synchronize()
             for c, (_, out, _) in zip(cases, parts):
                 c.check(out.cpu().numpy())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "fp8"])
+def test_calls_without_rows(kind):
+    """No tokens, rows or sequences (torch gives such tensors a null address): nothing is written and nothing fails.  A page
+    table without columns: zeros, and rows of a negative length stay."""
+    torch, q = torch_mod(), Q()
+    dtype = {"bf16": torch.bfloat16, "int8": torch.int8, "fp8": torch.uint8}[kind]
+    def none(*shape, dtype=torch.int16):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    ints = none(0, dtype=torch.int32)
+    cache = q.KVCache.empty(2, 2, 16, 64, dtype)
+    stored = [t for t in (cache.k, cache.v, cache.k_scale, cache.v_scale) if t is not None]
+    for t in stored:
+        t.view(torch.uint8).fill_(0x5A)
+    rope = q.Rope(64)
+    gamma = torch.zeros(64, dtype=torch.int16, device="cuda")
+    wide = torch.zeros(256, dtype=torch.int16, device="cuda")
+    codes, scales = none(0, 256, dtype=torch.int8), none(0, dtype=torch.float32)
+    q.qlin_norm_bf16(none(0, 256), wide, none(0, 256), residual=none(0, 256), sum_out=none(0, 256))
+    q.qlin_norm_int8(none(0, 256), wide, codes, scales)
+    q.qlin_norm_fp8(none(0, 256), wide, codes, scales)
+    q.qlin_norm_fp8(none(0, 256), wide, codes, none(0, 2, dtype=torch.float32), group=128)
+    q.qlin_rope(none(0, 4, 64), ints, rope, none(0, 4, 64), gamma=gamma)
+    q.qlin_cache_write(cache, ints, none(0, 2, 64), none(0, 2, 64), positions=ints, rope=rope, q=none(0, 4, 64), q_out=none(0, 4, 64),
+                       q_gamma=gamma, k_gamma=gamma)
+    q.qlin_cache_read(cache, ints, none(0, 2, 64), none(0, 2, 64))
+    work = none(q.qlin_attn_decode_workspace(4, cache), dtype=torch.uint8)
+    q.qlin_attn_decode(none(0, 4, 64), cache, none(0, 3, dtype=torch.int32), ints, none(0, 4, 64), work)
+    out = torch.full((3, 4, 64), 0x5A5A, dtype=torch.int16, device="cuda")
+    lengths = torch.tensor([7, -1, 0], dtype=torch.int32, device="cuda")
+    q.qlin_attn_decode(torch.zeros_like(out), cache, none(3, 0, dtype=torch.int32), lengths, out, work)
+    torch.cuda.synchronize()
+    assert not out[0].any() and bool((out[1] == 0x5A5A).all()) and not out[2].any()
+    for t in stored:
+        assert bool((t.view(torch.uint8) == 0x5A).all())
