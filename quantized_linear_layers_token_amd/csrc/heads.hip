@@ -256,7 +256,7 @@ void launch_tokens(const HeadsCall& c, hipStream_t st) {
 }
 // Several tokens to a workgroup where its threads hold their heads at once and
 // the workgroups are still many: 32768 tokens of one kv head of 64 channels
-// written in 5.1 us with 16, 32.0 with one.
+// written in 4.7 us with 16, 32.0 with one.
 template <int LANES, int KIND>
 void launch_lanes(const HeadsCall& c, hipStream_t st) {
     const int threads = (c.heads + 2 * c.kv_heads) * LANES;
