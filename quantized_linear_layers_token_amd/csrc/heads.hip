@@ -144,8 +144,8 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
             float amax = 0.0f;
             if constexpr (KIND != QLIN_CACHE_BF16) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-                amax = lanes_max<LANES>(amax);
+                for (int i = 0; i < 8; ++i) amax = larger(amax, fabsf(f[i]));
+                amax = lanes_absmax<LANES>(amax);
             }
             if (!mine || h >= all) continue;
             const int head = is_q ? h : h - a.heads - (is_v ? a.kv_heads : 0);

@@ -73,6 +73,11 @@ __device__ __forceinline__ v4u narrow8(const float (&f)[8]) {
     return v4u{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
 }
 
+// The larger of two magnitudes, NaN where one of them is: a row that holds a
+// NaN has to get a NaN scale, since int8 codes have none (fmaxf drops it).
+// One instruction for two of these.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Sum and maximum over runs of N = 8, 16 or 32 lanes; every lane gets the result.
 template <int N>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -91,6 +96,17 @@ __device__ __forceinline__ float lanes_max(float v) {
     if constexpr (N >= 16) v = fmaxf(v, dpp_f<0x140>(v));
     if constexpr (N >= 32) v = fmaxf(v, __shfl_xor(v, 16));
     return v;
+}
+// The largest of magnitudes, by the order of their bits, in which NaN is above all.
+template <int N>
+__device__ __forceinline__ float lanes_absmax(float a) {
+    uint32_t v = __float_as_uint(a);
+    v = max(v, (uint32_t)dpp_i<0xB1>((int)v));
+    v = max(v, (uint32_t)dpp_i<0x4E>((int)v));
+    v = max(v, (uint32_t)dpp_i<0x141>((int)v));
+    if constexpr (N >= 16) v = max(v, (uint32_t)dpp_i<0x140>((int)v));
+    if constexpr (N >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    return __uint_as_float(v);
 }
 
 }  // namespace qlin
