@@ -26,8 +26,9 @@
  *    on what else runs: the same call gives the same bits.
  *  - Inputs that are not finite, or past 2^55 in magnitude, give unspecified
  *    values in the rows (heads, sequences) that contain them and nowhere else.
- *    They do not vanish in 8 bits: the scale of a head that is rounded with a NaN
- *    or an infinity in it is NaN, and so is all that is read of the head.
+ *    They do not vanish in 8 bits: the scale of a head (token, group) that is
+ *    rounded with a NaN or an infinity in it is NaN, and so is all that is read
+ *    of it.
  */
 #ifndef QLIN_LAYER_H_
 #define QLIN_LAYER_H_

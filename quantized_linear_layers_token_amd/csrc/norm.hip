@@ -82,10 +82,10 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
         for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares);
         if constexpr (OUT != kNormBf16) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i] * w[i]));
+            for (int i = 0; i < 8; ++i) top = larger(top, fabsf(f[i] * w[i]));
         }
-        if constexpr (OUT == kNormFp8Block) group[j] = lanes_max<16>(top);   // 16 chunks: 128 inputs
-        else amax = fmaxf(amax, top);
+        if constexpr (OUT == kNormFp8Block) group[j] = lanes_absmax<16>(top);   // 16 chunks: 128 inputs
+        else amax = larger(amax, top);
     }
     squares = wave_sum_f32(squares);
     if constexpr (OUT == kNormInt8 || OUT == kNormFp8) amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(THREADS * ROWS) void norm_kernel(NormCall a) {
         __syncthreads();
         squares = red[0], amax = red[kWaves];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) squares += red[w], amax = fmaxf(amax, red[kWaves + w]);
+        for (int w = 1; w < kWaves; ++w) squares += red[w], amax = larger(amax, red[kWaves + w]);
     }
     const float d = 1.0f / sqrtf(squares / (float)a.K + a.eps);
 
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormCall a) {
         widen8(r, f);
         widen8(gamma[c], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares), amax = fmaxf(amax, fabsf(f[i] * w[i]));
+        for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(f[i], f[i], squares), amax = larger(amax, fabsf(f[i] * w[i]));
     }
     squares = wave_sum_f32(squares);
     amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormCall a) {
     __syncthreads();
     squares = red[0], amax = red[kWaves];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) squares += red[w], amax = fmaxf(amax, red[kWaves + w]);
+    for (int w = 1; w < kWaves; ++w) squares += red[w], amax = larger(amax, red[kWaves + w]);
     const float d = 1.0f / sqrtf(squares / (float)a.K + a.eps);
     Rounding rr = rounding<kFp8>(amax);
     if (OUT != kNormBf16 && OUT != kNormFp8Block && tid == 0) a.s[m] = scale_of<kFp8>(amax * d);
@@ -175,8 +175,8 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormCall a) {
         if constexpr (OUT == kNormFp8Block) {
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-            top = lanes_max<16>(top);
+            for (int i = 0; i < 8; ++i) top = larger(top, fabsf(f[i]));
+            top = lanes_absmax<16>(top);
             rr = rounding<true>(top);
             if (c < nchunks && c % 16 == 0) a.s[m * (a.K / 128) + c / 16] = scale_of<true>(top * d);
         }

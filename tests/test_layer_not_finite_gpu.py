@@ -1,5 +1,5 @@
-"""NaN and infinities in rows that are rounded to codes: the scale of the head that holds one is NaN, so that it shows in
-whatever reads the codes, and every other row has the bits that it has without them."""
+"""NaN and infinities in rows that are rounded to codes: the scale of the token (group, head) that holds one is NaN, so that
+it shows in whatever reads the codes, and every other row has the bits that it has without them."""
 import numpy as np
 import pytest
 
@@ -14,6 +14,45 @@ BAD = {"nan": 0x7FC0, "-nan": 0xFFC1, "inf": 0x7F80, "-inf": 0xFF80}
 def Q():
     import quantized_linear_layers_token_amd as q
     return q
+
+
+def same(a, b):
+    return np.array_equal(host(a).view(np.uint8), host(b).view(np.uint8))
+
+
+def norm(kind, x, gamma):
+    torch, q = torch_mod(), Q()
+    M, K = x.shape
+    codes = torch.empty((M, K), dtype=torch.int8 if kind == "int8" else torch.uint8, device="cuda")
+    s = torch.empty((M, K // 128) if kind == "block" else (M,), device="cuda")
+    if kind == "int8":
+        q.qlin_norm_int8(dev(x), dev(gamma), codes, s)
+    else:
+        q.qlin_norm_fp8(dev(x), dev(gamma), codes, s, group=128 if kind == "block" else 0)
+    return codes, s
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8", "block"])
+@pytest.mark.parametrize("K", [128, 512, 2048, 4096, 8192, 32768, 33280])     # every form of the kernel
+@pytest.mark.parametrize("bad", BAD)
+def test_norm(kind, K, bad):
+    rng = np.random.default_rng([1, K])
+    x, gamma = R.bits(rng.standard_normal((6, K))), R.bits(1 + 0.2 * rng.standard_normal(K))
+    codes, s = norm(kind, x, gamma)
+    assert np.isfinite(host(s)).all()
+    for row, channel in ((1, 0), (4, K - 1), (5, K // 2 + 3)):
+        y = x.copy()
+        y[row, channel] = BAD[bad]
+        got, t = norm(kind, y, gamma)
+        of_bad = host(t)[row, channel // 128] if kind == "block" else host(t)[row]
+        assert np.isnan(of_bad), (row, channel)
+        others = np.arange(6) != row
+        assert same(got[others], codes[others]) and same(t[others], s[others])
+    for channel in (0, K - 1):     # a weight of the norm: every row has it
+        g = gamma.copy()
+        g[channel] = BAD[bad]
+        t = host(norm(kind, x, g)[1])
+        assert np.isnan(t[:, channel // 128] if kind == "block" else t).all(), channel
 
 
 def written(kind, k, v, rope, positions, gamma, slots, pages, page):
