@@ -23,7 +23,7 @@ SOURCES = ["quant_act.hip", "gemv.hip", "gemm_small.hip", "gemm_large.hip", "gem
            "qlin_api.hip", "w4_stream.hip", "w4_tiled.hip", "route.hip", "experts.hip", "w4_api.hip",
            "norm.hip", "heads.hip", "attn_decode.hip", "layer_api.hip"]
 HEADERS = ["qlin_device.h", "qlin_internal.h", "qlin_round.h", "qlin_rows.h", "w4_device.h", "w4_internal.h", "layer_device.h",
-           "layer_internal.h", "attn_index.h"]
+           "layer_internal.h", "layer_forms.h", "attn_index.h"]
 
 # Never fast-math, never flush denormals: the quantizers are bit-exact against
 # IEEE f32 divide / multiply / round-half-even.  Packed FP32 instructions are

@@ -22,12 +22,13 @@
 #include <type_traits>
 
 #include "layer_device.h"
+#include "layer_forms.h"
 
 namespace qlin {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kHeadsThreads;
 constexpr int kAhead = 3;   // heads of each thread whose loads are under way together
 
 // Cosine and sine of position * frequency, times strength.  The product is
@@ -50,6 +51,7 @@ template <int LANES, int KIND, bool ROTATE, bool NEIGHBOURS, int TOKENS>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsCall a) {
     extern __shared__ float2 turns[];        // [TOKENS][dims / 2]
     constexpr int kPer = kThreads / LANES / TOKENS;   // heads of a token that the workgroup takes at once
+    static_assert(kPer > 0, "a token has a head");
     const int c = threadIdx.x % LANES, first = threadIdx.x / LANES % kPer;
     const int of = TOKENS > 1 ? threadIdx.x / LANES / kPer : 0;   // the thread's token
     const int64_t t = (int64_t)blockIdx.x * TOKENS + of;
@@ -246,29 +248,37 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(qlin_kv_cache a, c
     }
 }
 
-template <int LANES, int KIND, int TOKENS>
-void launch_tokens(const HeadsCall& c, hipStream_t st) {
-    const dim3 grid((unsigned)((c.T + TOKENS - 1) / TOKENS)), block(kThreads);
-    const size_t lds = c.rope.frequencies ? (size_t)TOKENS * (c.rope.dims / 2) * sizeof(float2) : 0;
-    if (!c.rope.frequencies) hipLaunchKernelGGL((heads_kernel<LANES, KIND, false, false, TOKENS>), grid, block, lds, st, c);
-    else if (c.rope.interleaved) hipLaunchKernelGGL((heads_kernel<LANES, KIND, true, true, TOKENS>), grid, block, lds, st, c);
-    else hipLaunchKernelGGL((heads_kernel<LANES, KIND, true, false, TOKENS>), grid, block, lds, st, c);
+template <int LANES, int KIND, bool ROTATE, bool NEIGHBOURS>
+void launch_form(const HeadsCall& c, hipStream_t st) {
+    constexpr bool kAlone = ROTATE && KIND == QLIN_CACHE_BF16;
+    auto go = [&](auto of) {
+        constexpr int kTokens = decltype(of)::value;
+        const size_t lds = ROTATE ? (size_t)kTokens * (c.rope.dims / 2) * sizeof(float2) : 0;
+        hipLaunchKernelGGL((heads_kernel<LANES, KIND, ROTATE, NEIGHBOURS, kTokens>), dim3((unsigned)((c.T + kTokens - 1) / kTokens)), dim3(kThreads), lds, st,
+                           c);
+    };
+    const int tokens = heads_tokens(LANES, c.heads + 2 * c.kv_heads, c.T);
+    if constexpr (heads_fit(16, LANES, kAlone)) {
+        if (tokens == 16) return go(std::integral_constant<int, 16>{});
+    }
+    if constexpr (heads_fit(4, LANES, kAlone)) {
+        if (tokens == 4) return go(std::integral_constant<int, 4>{});
+    }
+    go(std::integral_constant<int, 1>{});
 }
-// Several tokens to a workgroup where its threads hold their heads at once and
-// the workgroups are still many: 32768 tokens of one kv head of 64 channels
-// written in 4.7 us with 16, 32.0 with one.
 template <int LANES, int KIND>
 void launch_lanes(const HeadsCall& c, hipStream_t st) {
-    const int threads = (c.heads + 2 * c.kv_heads) * LANES;
-    if (16 * threads <= kThreads && c.T >= 8192) launch_tokens<LANES, KIND, 16>(c, st);
-    else if (4 * threads <= kThreads && c.T >= 1024) launch_tokens<LANES, KIND, 4>(c, st);
-    else launch_tokens<LANES, KIND, 1>(c, st);
+    if (!c.rope.frequencies) launch_form<LANES, KIND, false, false>(c, st);
+    else if (c.rope.interleaved) launch_form<LANES, KIND, true, true>(c, st);
+    else launch_form<LANES, KIND, true, false>(c, st);
 }
 template <int KIND>
 void launch_kind(const HeadsCall& c, hipStream_t st) {
-    if (c.dim <= 64) launch_lanes<8, KIND>(c, st);
-    else if (c.dim <= 128) launch_lanes<16, KIND>(c, st);
-    else launch_lanes<32, KIND>(c, st);
+    switch (heads_lanes(c.dim)) {
+        case 8: return launch_lanes<8, KIND>(c, st);
+        case 16: return launch_lanes<16, KIND>(c, st);
+        default: launch_lanes<32, KIND>(c, st);
+    }
 }
 
 }  // namespace

@@ -1,0 +1,5 @@
+// The rules of layer_forms.h for ctypes.
+#include "../../quantized_linear_layers_token_amd/csrc/layer_forms.h"
+
+extern "C" int heads_lanes(int dim) { return qlin::heads_lanes(dim); }
+extern "C" int heads_tokens(int lanes, int heads, int64_t T) { return qlin::heads_tokens(lanes, heads, T); }
