@@ -1,4 +1,5 @@
-"""The choice of the heads' kernel on the host: every form that the library holds is taken by some call."""
+"""The choice of the heads' kernel on the host: every form that the library holds is taken by some call, and by those of the
+GPU tests against the definition."""
 import ctypes
 import itertools
 import os
@@ -8,10 +9,11 @@ import subprocess
 
 import pytest
 
+import layer_forms as F
 import test_mfma_hazards as hazards
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-KINDS = ["bf16", "int8", "fp8"]
+KINDS = F.KINDS
 
 
 @pytest.fixture(scope="module")
@@ -51,4 +53,11 @@ def test_every_form_of_the_heads_kernel_is_taken(rules, tmp_path):
                 taken |= {heads_form(rules, kind, T, heads, kv_heads, dim, 16 * (turn > 0), turn == 2) for kind in KINDS}
             elif heads and turn:
                 taken.add(heads_form(rules, "bf16", T, heads, 0, dim, 16, turn == 2))
+    assert taken == built("heads.hip", "heads_kernel", tmp_path)
+
+
+def test_the_gpu_tests_take_every_form_of_the_heads_kernel(rules, tmp_path):
+    taken = {heads_form(rules, "bf16", T, heads, 0, dim, dims, interleaved) for T, heads, dim, dims, interleaved, _ in F.ROPE}
+    taken |= {heads_form(rules, kind, T, heads, kv_heads, dim, dims, interleaved)
+              for T, heads, kv_heads, dim, _, dims, interleaved, _ in F.WRITE for kind in KINDS}
     assert taken == built("heads.hip", "heads_kernel", tmp_path)
