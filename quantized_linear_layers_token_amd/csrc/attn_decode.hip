@@ -37,6 +37,7 @@
 
 #include "attn_index.h"
 #include "layer_device.h"
+#include "layer_forms.h"
 
 namespace qlin {
 
@@ -618,18 +619,14 @@ void launch_dim(const AttnArgs& a, bool alone, dim3 grid, hipStream_t st) {
 }
 template <int KIND>
 void launch_kind(const AttnArgs& a, bool alone, dim3 grid, hipStream_t st) {
-    if (a.dim <= 64) launch_dim<KIND, 64>(a, alone, grid, st);
-    else if (a.dim <= 128) launch_dim<KIND, 128>(a, alone, grid, st);
-    else launch_dim<KIND, 256>(a, alone, grid, st);
+    switch (attn_channels(a.dim)) {
+        case 64: return launch_dim<KIND, 64>(a, alone, grid, st);
+        case 128: return launch_dim<KIND, 128>(a, alone, grid, st);
+        default: launch_dim<KIND, 256>(a, alone, grid, st);
+    }
 }
 
-// An item is a sequence, and there is one launch, where no sequence can be
-// longer than two steps of a workgroup's wavefronts, or than kMedium and their
-// number fills half of the CUs; and for more sequences than a workgroup can scan.
-constexpr int64_t kMedium = 2048;
-constexpr int kScanned = 1024;
 constexpr int kMaxSequences = 4096;   // of a launch: up to 1024 groups of heads and 2^32 threads
-constexpr int kCus = 256;
 
 }  // namespace
 
@@ -682,8 +679,7 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     // two, 13.4 whole).
     a.least = c.S <= shape.workers / 2 ? kAttnWaves : 4 * kAttnWaves;
     a.scale = c.scale * 1.44269504088896340736f;
-    const int64_t tokens = (int64_t)c.columns * c.cache.page_size, whole = (int64_t)c.S * groups;
-    const bool alone = tokens <= (c.cache.dim <= 64 ? 512 : 256) || (tokens <= kMedium && whole >= kCus / 2) || c.S > kScanned;
+    const bool alone = attn_alone(c.S, (int64_t)c.columns * c.cache.page_size, groups, c.cache.dim);
     if (c.S > kMaxSequences) {   // one half of the sequences after the other
         AttnCall part = c;
         part.S = c.S / 2;

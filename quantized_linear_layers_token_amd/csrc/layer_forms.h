@@ -24,4 +24,19 @@ constexpr int heads_tokens(int lanes, int heads, int64_t T) {
 // rotated (in bf16), a key and a value otherwise.
 constexpr bool heads_fit(int tokens, int lanes, bool alone) { return tokens * lanes * (alone ? 1 : 2) <= kHeadsThreads; }
 
+constexpr int kCus = 256;
+
+// Channels of a head in the attention's registers.
+constexpr int attn_channels(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// An item is a sequence, and there is one launch, where no sequence of the
+// table's `tokens` can be longer than two steps of a workgroup's wavefronts, or
+// than kAttnMedium and the sequences' groups of heads fill half of the CUs; and
+// for more sequences than a workgroup can scan.
+constexpr int64_t kAttnMedium = 2048;
+constexpr int kAttnScanned = 1024;
+constexpr bool attn_alone(int64_t sequences, int64_t tokens, int groups, int dim) {
+    return tokens <= (dim <= 64 ? 512 : 256) || (tokens <= kAttnMedium && sequences * groups >= kCus / 2) || sequences > kAttnScanned;
+}
+
 }  // namespace qlin

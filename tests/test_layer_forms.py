@@ -1,5 +1,5 @@
-"""The choice of the heads' kernel on the host: every form that the library holds is taken by some call, and by those of the
-GPU tests against the definition."""
+"""The choice of the heads' and the attention's kernel on the host: every form that the library holds is taken by some call, and
+by those of the GPU tests against the definition."""
 import ctypes
 import itertools
 import os
@@ -26,6 +26,7 @@ def rules(tmp_path_factory):
     assert r.returncode == 0, r.stderr
     lib = ctypes.CDLL(out)
     lib.heads_tokens.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int64]
+    lib.attn_alone.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
     return lib
 
 
@@ -61,3 +62,27 @@ def test_the_gpu_tests_take_every_form_of_the_heads_kernel(rules, tmp_path):
     taken |= {heads_form(rules, kind, T, heads, kv_heads, dim, dims, interleaved)
               for T, heads, kv_heads, dim, _, dims, interleaved, _ in F.WRITE for kind in KINDS}
     assert taken == built("heads.hip", "heads_kernel", tmp_path)
+
+
+def attn_form(rules, kind, S, heads, kv_heads, dim, page, columns):
+    """-> kind, channels in registers, wavefronts, one launch."""
+    groups = kv_heads * -(-heads // kv_heads // 16)
+    channels, alone = rules.attn_channels(dim), rules.attn_alone(S, columns * page, groups, dim)
+    return KINDS.index(kind), channels, 8 if alone and channels == 64 else 4, alone
+
+
+def test_the_gpu_tests_take_every_form_of_the_attention(rules, tmp_path):
+    taken = {attn_form(rules, kind, len(lengths), *case, columns) for lengths, *case, columns, _ in F.ATTENTION for kind in KINDS}
+    assert taken == built("attn_decode.hip", "attn_kernel", tmp_path)
+
+
+def test_one_launch_by_each_of_its_rules(rules):
+    """The table is short; it is of a medium length and the workgroups many; the sequences are more than are scanned."""
+    for channels in (64, 128, 256):
+        short = 512 if channels == 64 else 256
+        cases = [(len(c[0]), c[4] * c[5], c[2] * -(-c[1] // c[2] // 16), c[3]) for c in F.ATTENTION if rules.attn_channels(c[3]) == channels]
+        assert any(tokens <= short for _, tokens, _, _ in cases)
+        medium = [c for c in cases if c[1] > short and rules.attn_alone(*c)]
+        assert medium and all(tokens <= 2048 and S * groups >= 128 for S, tokens, groups, _ in medium)
+        assert any(not rules.attn_alone(*c) for c in cases)
+    assert rules.attn_alone(1025, 1 << 20, 1, 128) and not rules.attn_alone(1024, 1 << 20, 1, 128)
