@@ -366,8 +366,10 @@ __global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP, KIND == QLIN_CACH
                     }
                 }
             }
-            // Single registers from here on: this compiler has lost the upper half of loaded pairs that were still to be
-            // used (the register allocator gave them to p), here and in no other form that was read or tested.
+            // Single registers from here on.  Without this clang 22 (ROCm 7.2) compiled an earlier state of this loop, in bf16
+            // for 64 channels in one launch, so that three loaded registers were given to p before their last use: 38 reads
+            // of them, an excerpt in tests/test_attn_lost_registers.py.  The loop as it is compiles to none either way, in
+            // the same time (no case by more than 0.2 %).
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
 #pragma unroll
