@@ -24,15 +24,15 @@
 // or there are a great many, an item is a sequence and there is one launch.
 //
 // Measured: 206744 tokens of 8 sequences (32 / 8 heads of 128, E4M3, 436 MB)
-// 85.8 us, 5.1 TB/s, the rate of a large copy; equal lengths 5.5 TB/s, bf16 5.9.
+// 85.9 us, 5.1 TB/s, the rate of a large copy; equal lengths 5.4 TB/s, bf16 5.7.
 // What is left of the time is fixed: 5 us for a short sequence in one launch
 // (lengths, page table and rows are three dependent loads), 2 for the second
 // launch, 1.5 to 2 more where it joins something.  A sequence of 777 tokens takes
-// 8.8 us, 37 ragged ones in bf16 (57 MB) 17.
-// Two units of every wavefront under way instead of one changed nothing
-// (101.3 -> 101.5 us for 8 x 32768 tokens) or cost up to a fifth (128 x 1024
-// tokens of 4 kv heads of 64: 16.8 -> 20.8), three workgroups to a CU instead of
-// two 5 %, eight wavefronts to a workgroup instead of four 40 % of 64 x 256 tokens.
+// 9.5 to 10 us (its kernels 7.2 and 3.0), 37 ragged ones in bf16 (57 MB) 17.
+// In earlier states of the loop two units of every wavefront under way instead
+// of one changed nothing (101.3 -> 101.5 us for 8 x 32768 tokens) or cost up to
+// a fifth (128 x 1024 tokens of 4 kv heads of 64: 16.8 -> 20.8), and eight
+// wavefronts to a workgroup instead of four 40 % of 64 x 256 tokens.
 #include <type_traits>
 
 #include "attn_index.h"
@@ -175,9 +175,9 @@ __device__ __forceinline__ unsigned scan(unsigned v) {
 }
 __device__ __forceinline__ unsigned lane_of(unsigned v, int lane) { return (unsigned)__builtin_amdgcn_readlane((int)v, lane); }
 
-// Wavefronts of a SIMD that the registers are bounded to.  Heads of 256
-// channels in 8 bits: 53 us with two (a few registers spilled), 77 with one, for
-// 16 x 4096 tokens of 16 / 8 heads; in bf16 122 and 119.
+// Wavefronts of a SIMD that the registers are bounded to; no form spills.  Heads
+// of 256 channels with two and with one, 16 x 4096 tokens of 16 / 8 heads: int8
+// 57.5 and 59.8 us, E4M3 56.9 and 56.3, bf16 108 (19 registers spilled) and 99.
 constexpr int waves_per_simd(int dp, bool bf16) { return dp == 64 ? 4 : dp == 128 ? 3 : bf16 ? 1 : 2; }
 
 // ALONE: a workgroup takes a whole sequence, and nothing is joined.
@@ -633,9 +633,10 @@ constexpr int kMaxSequences = 4096;   // of a launch: up to 1024 groups of heads
 }  // namespace
 
 AttnShape attn_shape(int heads, int kv_heads, int dim) {
-    // Two workgroups to a CU (one of 256 channels), though the registers hold more: 8 x 32768 tokens of 32 / 8 heads of
-    // 128 in E4M3 take 101 us with two to a CU, 109 with three or one.  The room that is left takes the items beyond
-    // `workers`, of which there are up to S.
+    // Two workgroups to a CU (one of 256 channels), though the registers hold more.  8 x 32768 tokens of 32 / 8 heads of
+    // 128 with one, two and three to a CU: E4M3 120, 103 and 106 us, int8 135, 106 and 109, bf16 188 each time.  16 x 4096
+    // of 256 channels in E4M3: 57.8, 57.6 and 63.0.  The room that is left takes the items beyond `workers`, of which there
+    // are up to S.
     const int share = kCus * (dim <= 128 ? 2 : 1);
     const int shared_by = heads / kv_heads, tiles = (shared_by + kAttnHeads - 1) / kAttnHeads;
     const int groups = kv_heads * tiles;
@@ -677,8 +678,9 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t st) {
     a.tiles = shape.tiles;
     a.rows = shape.rows;
     a.workers = shape.workers;
-    // Where the sequences are many, one of 512 tokens is not cut (64 of 256 tokens, 32 / 8 heads of 128: 18.2 us cut in
-    // two, 13.4 whole).
+    // Where the sequences are many, one of 512 tokens is not cut.  Since an item's size is looked for this matters little:
+    // 32 / 8 heads of 128 in E4M3 whole and cut down to 128 tokens, 64 x 256 tokens 13.2 us either way, 40 x 300 to 512
+    // 16.0 and 16.3, 63 x 1 to 512 15.8 and 16.2, 70 x 1 to 512 18.4 and 16.9.
     a.least = c.S <= shape.workers / 2 ? kAttnWaves : 4 * kAttnWaves;
     a.scale = c.scale * 1.44269504088896340736f;
     const bool alone = attn_alone(c.S, (int64_t)c.columns * c.cache.page_size, groups, c.cache.dim);

@@ -12,8 +12,8 @@
 // head of the token and stay in registers.
 //
 // Bound by memory for many tokens: 4096 tokens of 32 heads of 128, normalised
-// and rotated, 13.7 us (67 MB, 4.9 TB/s; without the norm 12.2); with 8 key and
-// value heads rounded to int8 as well 19 us (92 MB).  With eight channels of a
+// and rotated, 13.7 us (67 MB, 4.9 TB/s; without the norm 11.9); with 8 key and
+// value heads rounded to int8 as well 20 us (92 MB).  With eight channels of a
 // lane side by side, the partner's exchanged by LDS permutes and normalised a
 // second time, and two more divisions to a head, vector instructions bounded
 // it (17.7 and 29 us).  Rows read back: 65536 of 8 heads of 128 in E4M3, 77 us

@@ -10,12 +10,13 @@
 //
 // Bound by memory for many rows: 8192 x 4096 with the residual, E4M3 out,
 // moves 235 MB in 42 us (5.6 TB/s; a large copy reaches 5.1), and fetches and
-// writes exactly those bytes.  One row of 4096 takes 2.1 us above nothing else:
-// the call's host time (6.4 us) bounds it.  A row has the threads that hold it
+// writes exactly those bytes.  One row of 4096 takes 2.4 us: the call's host time
+// (6.3 to 6.9 us) bounds it.  A row has the threads that hold it
 // in one to four 16-byte chunks each: a wavefront up to 512 inputs (four rows
 // to a workgroup), 256 threads up to 8192, 1024 up to 32768, and two passes
-// over longer ones (131072 inputs, 256 rows: 45 us; held in registers, which
-// spill, 72).
+// over longer ones (256 rows of 131072 inputs into E4M3: 27 us, with the residual
+// 61; held in registers, which spill, 68 and 105.  Of 65536 inputs, which
+// registers would hold, 13.2 and 29.8 us, held 9.9 and 25.0).
 #include <type_traits>
 
 #include "layer_device.h"
