@@ -30,15 +30,25 @@ def rules(tmp_path_factory):
     return lib
 
 
-def built(source, kernel, tmp_path):
-    """Template arguments of every form of a kernel, from the assembly of the source as the library is built from it."""
+@pytest.fixture(scope="module")
+def built(tmp_path_factory):
+    """Of a source and a kernel: the template arguments of every form, from the assembly as the library is built from it."""
     b = hazards._load_build()
-    if not os.path.exists(b.hipcc()):
+    try:
+        hipcc = b.hipcc()
+    except RuntimeError:
         pytest.skip("hipcc is not installed")
-    text = hazards._asm(source, str(tmp_path), [f for f in b.CFLAGS if f != "-fPIC"], b.hipcc())
-    forms = re.findall(rf"^_ZN4qlin12_GLOBAL__N_1{len(kernel)}{kernel}I((?:L[ib]\d+E)+)E\S*:", text, re.M)
-    assert forms
-    return {tuple(int(v) for v in re.findall(r"L[ib](\d+)E", f)) for f in forms}
+    found = {}
+
+    def of(source, kernel):
+        if source not in found:
+            text = hazards._asm(source, str(tmp_path_factory.mktemp("asm")), [f for f in b.CFLAGS if f != "-fPIC"], hipcc)
+            forms = re.findall(rf"^_ZN4qlin12_GLOBAL__N_1{len(kernel)}{kernel}I((?:L[ib]\d+E)+)E\S*:", text, re.M)
+            assert forms
+            found[source] = {tuple(int(v) for v in re.findall(r"L[ib](\d+)E", f)) for f in forms}
+        return found[source]
+
+    return of
 
 
 def heads_form(rules, kind, T, heads, kv_heads, dim, dims, interleaved):
@@ -46,7 +56,7 @@ def heads_form(rules, kind, T, heads, kv_heads, dim, dims, interleaved):
     return lanes, KINDS.index(kind), int(dims > 0), int(dims > 0 and interleaved), rules.heads_tokens(lanes, heads + 2 * kv_heads, T)
 
 
-def test_every_form_of_the_heads_kernel_is_taken(rules, tmp_path):
+def test_every_form_of_the_heads_kernel_is_taken(rules, built):
     taken = set()
     for T, dim, kv_heads, heads in itertools.product((1, 1023, 1024, 8191, 8192, 1 << 24), range(16, 257, 16), (0, 1, 2, 8), (0, 1, 2, 3, 8, 32)):
         for turn in (0, 1, 2):      # none, halves, neighbours
@@ -54,14 +64,14 @@ def test_every_form_of_the_heads_kernel_is_taken(rules, tmp_path):
                 taken |= {heads_form(rules, kind, T, heads, kv_heads, dim, 16 * (turn > 0), turn == 2) for kind in KINDS}
             elif heads and turn:
                 taken.add(heads_form(rules, "bf16", T, heads, 0, dim, 16, turn == 2))
-    assert taken == built("heads.hip", "heads_kernel", tmp_path)
+    assert taken == built("heads.hip", "heads_kernel")
 
 
-def test_the_gpu_tests_take_every_form_of_the_heads_kernel(rules, tmp_path):
+def test_the_gpu_tests_take_every_form_of_the_heads_kernel(rules, built):
     taken = {heads_form(rules, "bf16", T, heads, 0, dim, dims, interleaved) for T, heads, dim, dims, interleaved, _ in F.ROPE}
     taken |= {heads_form(rules, kind, T, heads, kv_heads, dim, dims, interleaved)
               for T, heads, kv_heads, dim, _, dims, interleaved, _ in F.WRITE for kind in KINDS}
-    assert taken == built("heads.hip", "heads_kernel", tmp_path)
+    assert taken == built("heads.hip", "heads_kernel")
 
 
 def attn_form(rules, kind, S, heads, kv_heads, dim, page, columns):
@@ -71,9 +81,9 @@ def attn_form(rules, kind, S, heads, kv_heads, dim, page, columns):
     return KINDS.index(kind), channels, 8 if alone and channels == 64 else 4, alone
 
 
-def test_the_gpu_tests_take_every_form_of_the_attention(rules, tmp_path):
+def test_the_gpu_tests_take_every_form_of_the_attention(rules, built):
     taken = {attn_form(rules, kind, len(lengths), *case, columns) for lengths, *case, columns, _ in F.ATTENTION for kind in KINDS}
-    assert taken == built("attn_decode.hip", "attn_kernel", tmp_path)
+    assert taken == built("attn_decode.hip", "attn_kernel")
 
 
 def test_one_launch_by_each_of_its_rules(rules):
