@@ -176,8 +176,10 @@ int64_t qlin_attn_decode_workspace(int32_t heads, int32_t kv_heads, int32_t dim)
  *     tokens of a page outside the cache are left out of the softmax (none
  *     left: zero).
  * q, out bf16 [S, heads, dim], 16-byte aligned, out overlapping nothing.
- * Products q . k are exact, sums f32; p * v_scale is a matrix-core operand and
- * kept as two bf16 parts (16 bits).  page_columns * page_size is at most 2^30.
+ * Products q . k are exact, sums f32; p * v_scale (p of at most 1, before it is
+ * divided by its sum) is a matrix-core operand and kept as two bf16 parts: off
+ * by 2^-17 of it or by 2^-134, which is more below 2^-117.
+ * page_columns * page_size is at most 2^30.
  * workspace: qlin_attn_decode_workspace bytes, 16-byte aligned; its contents
  * before and after a call mean nothing.  Calls that may run at the same time
  * need workspaces of their own. */

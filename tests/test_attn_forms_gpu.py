@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import layer_forms as F
+import layer_reference as R
 import test_attn_gpu as A
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +44,19 @@ def test_masked_places_hold_anything(kind, dim, columns):
             s[dead & (np.arange(c.page) % 3 == 0)[None]] = np.inf
     c.load()
     c.check(c.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("exponent", [-110, -117, -120, -123, -126])
+def test_small_value_scales(kind, exponent):
+    """Scales of values near the end of the f32 range: a product p * v_scale is off by 2^-134 at most besides its relative
+    error (half a step of a subnormal bf16), times a code, over the tokens; the sums and the output, half a step of their
+    subnormals (2^-150 and 2^-134)."""
+    c = A.Case(23, kind, [300, 33], 4, 2, 64, 16)
+    scales = np.ldexp(c.scales["v"].astype(np.float64) * 32, exponent)
+    c.scales["v"] = scales.astype(np.float32)
+    y = R.value(c.load().run())
+    ref, room = R.attention(R.value(c.q), c.values("k"), c.values("v"), c.table, c.lengths, c.page, 0, float(np.float32(64 ** -0.5)))
+    tokens = np.array(c.lengths)[:, None, None]
+    room = room + tokens * (2.0 ** -134 * R.MOST[kind] + 4 * 2.0 ** -150) + 2.0 ** -134
+    assert (np.abs(y - ref) <= np.abs(ref) * R.HALF + room * (1 + R.HALF)).all()
