@@ -366,10 +366,10 @@ __global__ __launch_bounds__(WAVES * kWave, waves_per_simd(DP, KIND == QLIN_CACH
                     }
                 }
             }
-            // Single registers from here on.  Without this clang 22 (ROCm 7.2) compiled an earlier state of this loop, in bf16
-            // for 64 channels in one launch, so that three loaded registers were given to p before their last use: 38 reads
-            // of them, an excerpt in tests/test_attn_lost_registers.py.  The loop as it is compiles to none either way, in
-            // the same time (no case by more than 0.2 %).
+            // Single registers from here on.  Without this clang 22 (ROCm 7.2) compiled an earlier state of this loop, in the
+            // three one-launch forms for bf16, so that loaded registers were given to p before their last use: 6, 16 and 16
+            // reads of them, an excerpt in tests/test_attn_lost_registers.py.  The loop as it is compiles to none either way,
+            // in the same time (no case by more than 0.2 %).
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
 #pragma unroll

@@ -1,11 +1,11 @@
-"""The scan for lost registers (test_layer_host.py) on assembly in which the compiler lost some: excerpts of the attention's
+"""The scan for lost registers (test_layer_host.py) on assembly in which the compiler lost some: an excerpt of the attention's
 one-launch form for bf16 and 64 channels, as clang 22 of ROCm 7.2 compiled an earlier state of its loop without the empty asm
 statement that its values pass through now."""
 from test_layer_host import lost_registers
 
 NAME = "_ZN4qlin12_GLOBAL__N_111attn_kernelILi0ELi64ELi8ELb1EEEvNS0_8AttnArgsE:\n"
 
-# Three of 38: v77, v71 and v74 are the second dwords of three tokens' values (s[4:5] .. s[8:9]: live tokens); v71 becomes the
+# v77, v71 and v74 are the second dwords of three tokens' values (s[4:5] .. s[8:9]: live tokens); v71 becomes the
 # maximum, v77 and v74 what is left of two p; the byte permutations read all three as values.
 LOST = """
 	v_mfma_f32_16x16x32_bf16 v[42:45], v[10:13], v[2:5], v[86:89]
